@@ -244,9 +244,9 @@ def _frequencies(rotary, scaling):
 
 
 # ----------------------------------------------------------------- the inputs
-def _vectors(g, shape):
+def _vectors(g, shape, spread=1.0):
     """N(0, 1) times a log-normal scale of each (head, channel)."""
-    w = torch.randn(shape[-2:], generator=g, device="cuda")
+    w = spread * torch.randn(shape[-2:], generator=g, device="cuda")
     return torch.randn(shape, generator=g, device="cuda") * torch.exp(w)
 
 
@@ -350,8 +350,10 @@ def prepare(case, seed):
         units, capacity, table = _paged(case, slots, g)
         cache = _cache(case, units, capacity)
         s["q"] = torch.randn(batch, n, case["hq"], d, generator=g, device="cuda").to(DTYPES[case["dtype"]])
-        s["k"] = _vectors(g, (batch, n, case["hkv"], d)).to(DTYPES[case["dtype"]])
-        s["v"] = _vectors(g, (batch, n, case["hkv"], d)).to(DTYPES[case["dtype"]])
+        # (half the spread of a cache's history: where one channel of a narrow head outweighs the rest, all its rotated
+        # coordinates lie at one distance from a code's border, and any rounding moves them all)
+        s["k"] = _vectors(g, (batch, n, case["hkv"], d), 0.5).to(DTYPES[case["dtype"]])
+        s["v"] = _vectors(g, (batch, n, case["hkv"], d), 0.5).to(DTYPES[case["dtype"]])
         # slots in a window of the cache; positions as of a context that began far earlier, one depth of a tree
         # holding several of them
         s["at"] = torch.randint(0, slots - n + 1, (batch,), generator=g, device="cuda").to(torch.int32)
