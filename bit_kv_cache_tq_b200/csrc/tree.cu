@@ -1,0 +1,470 @@
+// Attention of a tree of drafted tokens over the cache: the general kernel,
+// and the C entry points.
+//
+// For draft t of sequence b and query head h (kv head h / (Hq / Hkv)):
+//   s_i = sm_scale <q, k_hat_i>,  p = softmax over the slots the draft sees,
+//   out = sum_i p_i v_hat_i,
+// where the draft sees the base[b] slots before the tree and the drafts its
+// mask names.  Turbo keys score in the rotated domain, n_i <R q, c[code]>, and
+// turbo values are summed there, with one inverse rotation at the end; int8
+// sides stay in the original domain.  A key's sketch enters the score product
+// as m more channels: the key row carries +-gamma in them, the query row
+// sqrt(pi/2)/m (S R q).
+//
+// The general kernel takes every configuration: 64 query rows (16 a warp) of
+// one (sequence, kv head) against tiles of BK keys, dequantised to fp16 in
+// shared memory; warp-level MMAs (m16n8k16, fp32 accumulation); the online
+// softmax in registers.  Queries enter as two fp16 terms, so a score keeps
+// about 22 bits of its query.  The key axis is split between blocks and the
+// merge kernel joins the pieces.
+
+#include "tree_common.cuh"
+
+namespace tq {
+namespace tree {
+
+constexpr int GEN_ROWS = 64, GEN_THREADS = 128;
+// weights are held as 2^(s - m + PSHIFT) <= 2^12 in fp16: those 2^26 times
+// smaller than the largest are still normal numbers
+constexpr float PSHIFT = 12.0f;
+
+template <int D>
+constexpr int GEN_BK = D == 256 ? 32 : 64;
+
+// Rows of halves padded by 8, so that the 8 rows of a fragment load fall in different banks.
+__host__ __device__ constexpr int gen_qk_stride(int d, int m) { return d + m + 8; }
+template <int D>
+constexpr size_t gen_smem(int m) {
+    return (2ull * GEN_ROWS + GEN_BK<D>) * gen_qk_stride(D, m) * 2 + GEN_BK<D> * (D + 8) * 2ull +
+           GEN_BK<D> * 4ull + GEN_ROWS * 4ull + 128;
+}
+
+__device__ __forceinline__ void ldmatrix_x2_trans(uint32_t& r0, uint32_t& r1, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
+}
+
+template <int D>
+__global__ void __launch_bounds__(GEN_THREADS) tree_general_kernel(const __grid_constant__ Args a) {
+    constexpr int BK = GEN_BK<D>, LPV = D / 32, VPW = 32 / LPV;
+    extern __shared__ __align__(16) uint8_t gsm[];
+    const int m = a.qjl_dims, KD = D + m, KS = gen_qk_stride(D, m), VS = D + 8;
+    __half* qh = reinterpret_cast<__half*>(gsm);
+    __half* ql = qh + GEN_ROWS * KS;
+    __half* ks = ql + GEN_ROWS * KS;
+    __half* vs = ks + BK * KS;
+    float* kn = reinterpret_cast<float*>(vs + BK * VS);
+    float* qscale = kn + BK;
+    float* cent = qscale + GEN_ROWS;  // key centroids (key_scale c), then value centroids (sqrt(d)/4 c)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % LPV, grp = lane / LPV;
+    if (tid < 32) cent[tid] = tid < 16 ? a.kcent32[tid] : a.vcent32[tid - 16];
+    const Unit x = unit_of<BK>(a, static_cast<int>(blockIdx.x));
+    const int G = a.group, split = static_cast<int>(blockIdx.y);
+    float* mine = a.parts + (static_cast<size_t>(blockIdx.x) * a.n_split + split) * (GEN_ROWS * (D + 2));
+    const int j0 = static_cast<int>(static_cast<long long>(x.ntiles) * split / a.n_split);
+    const int j1 = static_cast<int>(static_cast<long long>(x.ntiles) * (split + 1) / a.n_split);
+    if (x.bad && x.qt == 0 && x.kv == 0 && split == 0 && tid == 0 && a.err) atomicOr(a.err, TQ_DEVERR_SEQLEN);
+    if (j1 <= j0) {
+        if (tid < GEN_ROWS) mine[GEN_ROWS * D + tid] = -INFINITY;
+        return;
+    }
+    // ---- queries: rotated (turbo keys), the sketch's projections appended,
+    // scaled to a largest magnitude of 1, as fp16 hi + lo
+    for (int base = warp * VPW; base < GEN_ROWS; base += (GEN_THREADS / 32) * VPW) {
+        const int r = base + grp, t = r / G, g = r % G;
+        const bool in = t < x.ntok;
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (in) {
+                const size_t off = ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + t) * a.hq + x.kv * G + g) * D +
+                                   8 * (sub + LPV * k);
+                float (&lo)[4] = *reinterpret_cast<float (*)[4]>(&v[8 * k]);
+                float (&hi)[4] = *reinterpret_cast<float (*)[4]>(&v[8 * k + 4]);
+                load4(a.q, off, a.q_dtype, lo);
+                load4(a.q, off + 4, a.q_dtype, hi);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[8 * k + e] = 0.f;
+            }
+        }
+        if (a.k_bits != 8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[8 * k + e] = flip_sign(v[8 * k + e], sign_bit(a.signs, 8 * (sub + LPV * k) + e));
+            fwht_registers(v);
+            fwht_lanes<32, LPV>(v, sub);
+            const float rs = rsqrtf(static_cast<float>(D));
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= rs;
+        }
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) big = fmaxf(big, fabsf(v[i]));
+        // the sketch's projections, twice: for the row's scale, then stored
+        // with it.  A key channel is centroid x key_scale, a sketch channel
+        // +-gamma: the projections carry the scale instead.
+        const float coef = m ? sqrtf(0.5f * 3.14159265358979f) / m * a.key_scale : 0.f;
+        auto project = [&](int j) {
+            const float* row = a.sketch + static_cast<size_t>(j) * D;
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(__ldg(row + 8 * (sub + LPV * k) + e), v[8 * k + e], s);
+            return group_sum<LPV>(s) * coef;
+        };
+        for (int j = 0; j < m; ++j) big = fmaxf(big, fabsf(project(j)));
+        big = group_max<LPV>(big);
+        const float inv = big > 0.f ? 1.f / big : 0.f;
+        auto put = [&](int c, float y) {
+            const __half h = __float2half_rn(y);
+            qh[r * KS + c] = h;
+            ql[r * KS + c] = __float2half_rn(y - __half2float(h));
+        };
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) put(8 * (sub + LPV * k) + e, v[8 * k + e] * inv);
+        for (int j = 0; j < m; ++j) {
+            const float s = project(j);
+            if (sub == 0) put(D + j, s * inv);
+        }
+        if (sub == 0) qscale[r] = big;
+    }
+    __syncthreads();
+    const int r0 = warp * 16 + lane / 4, r1 = r0 + 8;  // the lane's two rows
+    const float rs0 = qscale[r0] * a.score_scale, rs1 = qscale[r1] * a.score_scale;
+    const uint64_t mk0 = r0 / G < x.ntok ? row_mask(a, x, x.tok0 + r0 / G) : 0ull;
+    const uint64_t mk1 = r1 / G < x.ntok ? row_mask(a, x, x.tok0 + r1 / G) : 0ull;
+    float o[D / 8][4], m0 = NOTHING, m1 = NOTHING, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[i][q] = 0.f;
+    const int kbytes = a.k_bits == 8 ? D : D * a.k_bits / 8, vbytes = a.v_bits == 8 ? D : D * a.v_bits / 8;
+
+    for (int j = j0; j < j1; ++j) {
+        const int key0 = j * BK, nk = min(BK, x.kend - key0);
+        // ---- the tile to fp16: keys as centroids (norms multiply the fp32
+        // scores), values times their norms; slots past the end are zeros
+        for (int i = tid; i < 2 * BK * (D / 8); i += GEN_THREADS) {
+            const bool isv = i >= BK * (D / 8);
+            const int w = isv ? i - BK * (D / 8) : i, key = w / (D / 8), c = w % (D / 8);
+            const int bits = isv ? a.v_bits : a.k_bits, rb = isv ? vbytes : kbytes;
+            uint4 h = make_uint4(0u, 0u, 0u, 0u);
+            if (key < nk) {
+                const size_t row = cache_row(a, x.b, x.kv, key0 + key);
+                const uint8_t* src = (isv ? a.v_codes : a.k_codes) + row * rb;
+                // (a value row that is not finite is left out of V~, where a
+                // zero weight would turn it into NaN for rows that do not see
+                // it; its key's score is NaN instead, for those that do)
+                const float vn = half_bits_to_float(a.v_norms[row]);
+                const bool fine = fabsf(vn) < INFINITY;
+                const float n = isv ? (fine ? vn : 0.f) : 1.f;
+                float y[8];
+                if (bits == 8) {
+                    const uint2 b8 = *reinterpret_cast<const uint2*>(src + 8 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = n * static_cast<float>(
+                                       static_cast<int8_t>(((e < 4 ? b8.x : b8.y) >> (8 * (e & 3))) & 0xffu));
+                } else {
+                    const uint32_t codes = stream_bits(reinterpret_cast<const uint32_t*>(src), rb / 4, 8 * bits * c, 8 * bits);
+                    const float* ct = cent + (isv ? 16 : 0);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = n * ct[(codes >> (bits * e)) & ((1u << bits) - 1u)];
+                }
+                h = make_uint4(ptx::pack_half2(y[0], y[1]), ptx::pack_half2(y[2], y[3]), ptx::pack_half2(y[4], y[5]),
+                               ptx::pack_half2(y[6], y[7]));
+                if (!isv && c == 0) kn[key] = fine ? half_bits_to_float(a.k_norms[row]) : NAN;
+            } else if (!isv && c == 0) {
+                kn[key] = 0.f;
+            }
+            *reinterpret_cast<uint4*>(isv ? vs + key * VS + 8 * c : ks + key * KS + 8 * c) = h;
+        }
+        for (int i = tid; i < BK * (m / 32); i += GEN_THREADS) {  // the sketch's channels: +-gamma
+            const int key = i / (m / 32), w = i % (m / 32);
+            uint32_t z = 0;
+            uint16_t gm = 0;
+            if (key < nk) {
+                const size_t row = cache_row(a, x.b, x.kv, key0 + key);
+                z = reinterpret_cast<const uint32_t*>(a.k_qjl + row * (m / 8))[w];
+                gm = a.k_gamma[row];
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                const uint32_t lo = gm ^ (((z >> e) & 1u) ? 0u : 0x8000u), hi = gm ^ (((z >> (e + 1)) & 1u) ? 0u : 0x8000u);
+                *reinterpret_cast<uint32_t*>(ks + key * KS + D + 32 * w + e) = lo | (hi << 16);
+            }
+        }
+        __syncthreads();
+        // ---- scores
+        float s[BK / 8][4];
+#pragma unroll
+        for (int n = 0; n < BK / 8; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s[n][q] = 0.f;
+        for (int c = 0; c < KD; c += 16) {
+            const int cc = c + 2 * (lane & 3);
+            auto w32 = [](const __half* p) { return *reinterpret_cast<const uint32_t*>(p); };
+            const uint32_t h0 = w32(qh + r0 * KS + cc), h1 = w32(qh + r1 * KS + cc), h2 = w32(qh + r0 * KS + cc + 8),
+                           h3 = w32(qh + r1 * KS + cc + 8);
+            const uint32_t g0 = w32(ql + r0 * KS + cc), g1 = w32(ql + r1 * KS + cc), g2 = w32(ql + r0 * KS + cc + 8),
+                           g3 = w32(ql + r1 * KS + cc + 8);
+#pragma unroll
+            for (int n = 0; n < BK / 8; ++n) {
+                const __half* kp = ks + (8 * n + lane / 4) * KS + cc;
+                const uint32_t b0 = w32(kp), b1 = w32(kp + 8);
+                ptx::mma_16816(s[n], h0, h1, h2, h3, b0, b1);
+                ptx::mma_16816(s[n], g0, g1, g2, g3, b0, b1);
+            }
+        }
+        // ---- online softmax, in log2 units
+        const uint64_t v0 = visible(mk0, key0, x.base), v1 = visible(mk1, key0, x.base);
+        float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < BK / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int key = 8 * n + 2 * (lane & 3) + e;
+                const float kk = kn[key];
+                s[n][e] = key < nk && ((v0 >> key) & 1u) ? s[n][e] * kk * rs0 : -INFINITY;
+                s[n][2 + e] = key < nk && ((v1 >> key) & 1u) ? s[n][2 + e] * kk * rs1 : -INFINITY;
+                t0 = fmaxf(t0, s[n][e]);
+                t1 = fmaxf(t1, s[n][2 + e]);
+            }
+#pragma unroll
+        for (int q = 1; q < 4; q <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(kFullMask, t0, q));
+            t1 = fmaxf(t1, __shfl_xor_sync(kFullMask, t1, q));
+        }
+        const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+        const float c0 = ptx::ex2(m0 - n0), c1 = ptx::ex2(m1 - n1);
+        const float f0 = PSHIFT - n0, f1 = PSHIFT - n1;
+        m0 = n0;
+        m1 = n1;
+        l0 *= c0;
+        l1 *= c1;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= c0;
+            o[i][1] *= c0;
+            o[i][2] *= c1;
+            o[i][3] *= c1;
+        }
+#pragma unroll
+        for (int n = 0; n < BK / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                s[n][e] = ptx::ex2(s[n][e] + f0);
+                s[n][2 + e] = ptx::ex2(s[n][2 + e] + f1);
+                l0 += s[n][e];
+                l1 += s[n][2 + e];
+            }
+        // ---- O += P V
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint32_t a0 = ptx::pack_half2(s[2 * kk][0], s[2 * kk][1]), a1 = ptx::pack_half2(s[2 * kk][2], s[2 * kk][3]);
+            const uint32_t a2 = ptx::pack_half2(s[2 * kk + 1][0], s[2 * kk + 1][1]),
+                           a3 = ptx::pack_half2(s[2 * kk + 1][2], s[2 * kk + 1][3]);
+            const uint32_t vrow = ptx::smem_addr(vs + (16 * kk + (lane & 15)) * VS);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                uint32_t b0, b1;
+                ldmatrix_x2_trans(b0, b1, vrow + 16 * i);
+                ptx::mma_16816(o[i], a0, a1, a2, a3, b0, b1);
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int q = 1; q < 4; q <<= 1) {
+        l0 += __shfl_xor_sync(kFullMask, l0, q);
+        l1 += __shfl_xor_sync(kFullMask, l1, q);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+        *reinterpret_cast<float2*>(mine + r0 * D + 8 * i + 2 * (lane & 3)) = make_float2(o[i][0], o[i][1]);
+        *reinterpret_cast<float2*>(mine + r1 * D + 8 * i + 2 * (lane & 3)) = make_float2(o[i][2], o[i][3]);
+    }
+    if ((lane & 3) == 0) {
+        mine[GEN_ROWS * D + r0] = piece_reference(m0, l0);
+        mine[GEN_ROWS * D + r1] = piece_reference(m1, l1);
+        mine[GEN_ROWS * (D + 1) + r0] = l0;
+        mine[GEN_ROWS * (D + 1) + r1] = l1;
+    }
+}
+
+// One warp per query row: block (unit, 8 rows).
+constexpr int MERGE_THREADS = 256;
+template <int D>
+__global__ void __launch_bounds__(MERGE_THREADS) tree_general_merge_kernel(const __grid_constant__ Args a) {
+    const Unit x = unit_of<GEN_BK<D>>(a, static_cast<int>(blockIdx.x));
+    const int r = static_cast<int>(blockIdx.y) * (MERGE_THREADS / 32) + (static_cast<int>(threadIdx.x) >> 5);
+    const int G = a.group, t = r / G, g = r % G;
+    // rows past the sequence's drafts are left as they are (all n_draft rows of a refused sequence are zeros)
+    const int rows = x.bad ? min(a.tok_per_tile, a.n_draft - x.tok0) : x.ntok;
+    if (t >= rows) return;
+    const float* first = a.parts + static_cast<size_t>(blockIdx.x) * a.n_split * (GEN_ROWS * (D + 2));
+    const size_t dst = ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + t) * a.hq + x.kv * G + g) * D;
+    merge_row<D, GEN_ROWS>(
+        a, [&](int j) { return first + static_cast<size_t>(j) * (GEN_ROWS * (D + 2)); }, x.bad ? 0 : a.n_split, r, dst,
+        true);
+}
+
+struct Plan {
+    long long units;
+    int tok_per_tile, qtiles, n_split;
+    size_t bytes;
+};
+
+static Plan general_plan(const tq_params& p, int batch, int n_draft, int sms) {
+    Plan pl{};
+    pl.tok_per_tile = GEN_ROWS / (p.num_q_heads / p.num_kv_heads);
+    pl.qtiles = (n_draft + pl.tok_per_tile - 1) / pl.tok_per_tile;
+    pl.units = static_cast<long long>(batch) * p.num_kv_heads * pl.qtiles;
+    // about three blocks an SM (what shared memory lets reside), fewer when the units alone fill them
+    long long n = (3ll * sms + pl.units - 1) / pl.units;
+    pl.n_split = static_cast<int>(n < 1 ? 1 : n > 256 ? 256 : n);
+    pl.bytes = static_cast<size_t>(pl.units) * pl.n_split * GEN_ROWS * (p.head_dim + 2) * sizeof(float);
+    return pl;
+}
+
+template <int D>
+static cudaError_t launch_general(const Args& a, cudaStream_t s) {
+    const size_t smem = gen_smem<D>(a.qjl_dims);
+    cudaError_t e = cudaFuncSetAttribute(tree_general_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    tree_general_kernel<D><<<dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(a.n_split)), GEN_THREADS, smem, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    tree_general_merge_kernel<D><<<dim3(static_cast<unsigned>(a.units), GEN_ROWS / (MERGE_THREADS / 32)), MERGE_THREADS, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+static tq_status attend(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const void* d_q,
+                        tq_dtype q_dtype, int32_t n_draft, const uint64_t* d_mask, const int32_t* d_base,
+                        const int32_t* d_draft_lens, const tq_cache* cache, const PageMap* pm, void* d_out,
+                        tq_dtype out_dtype, void* d_workspace, size_t workspace_bytes, uint32_t* d_error,
+                        void* stream) {
+    tq_status st = validate_params(params);
+    if (st != TQ_OK) return st;
+    const tq_params& p = *params;
+    if ((st = validate_cache(p, cache)) != TQ_OK) return st;
+    if (!d_q || !d_out || !d_mask || !d_base || n_draft < 1) return TQ_ERR_INVALID_ARG;
+    for (const tq_dtype t : {q_dtype, out_dtype})
+        if (t != TQ_F32 && t != TQ_BF16 && t != TQ_F16) return TQ_ERR_INVALID_ARG;
+    if (n_draft > MAX_DRAFTS) return TQ_ERR_UNSUPPORTED;
+    if (!aligned16(d_q) || !aligned16(d_out)) return TQ_ERR_ALIGNMENT;
+    if (p.k_mode == TQ_MODE_TURBO && (st = validate_codebook(kcb, p.head_dim, p.k_bits)) != TQ_OK) return st;
+    if (p.v_mode == TQ_MODE_TURBO && (st = validate_codebook(vcb, p.head_dim, p.v_bits)) != TQ_OK) return st;
+    const int batch = pm ? pm->batch : cache->batch;
+    const int sms = num_sms_current();
+    if (sms <= 0) return TQ_ERR_CUDA;
+    const Plan pl = general_plan(p, batch, n_draft, sms);
+    if (pl.units > INT32_MAX) return TQ_ERR_INVALID_ARG;
+    if (!d_workspace) return TQ_ERR_INVALID_ARG;
+    if (workspace_bytes < pl.bytes) return TQ_ERR_CAPACITY;
+    if (!aligned16(d_workspace)) return TQ_ERR_ALIGNMENT;
+    Args a{};
+    a.k_codes = cache->k_codes;
+    a.v_codes = cache->v_codes;
+    a.k_norms = cache->k_norms;
+    a.v_norms = cache->v_norms;
+    a.k_qjl = cache->k_qjl;
+    a.k_gamma = cache->k_gamma;
+    a.sketch = cache->qjl_matrix;
+    a.q = d_q;
+    a.mask = d_mask;
+    a.base = d_base;
+    a.draft_lens = d_draft_lens;
+    a.out = d_out;
+    a.err = d_error;
+    a.parts = static_cast<float*>(d_workspace);
+    a.capacity = pm ? pm->max_blocks * pm->block_size : cache->capacity;
+    if (pm) {
+        a.table = pm->table;
+        a.max_blocks = pm->max_blocks;
+        a.block_size = pm->block_size;
+        a.num_blocks = pm->num_blocks;
+    }
+    a.q_dtype = q_dtype;
+    a.out_dtype = out_dtype;
+    a.batch = batch;
+    a.hq = p.num_q_heads;
+    a.hkv = p.num_kv_heads;
+    a.group = p.num_q_heads / p.num_kv_heads;
+    a.n_draft = n_draft;
+    a.k_bits = p.k_mode == TQ_MODE_INT8 ? 8 : p.k_bits;
+    a.v_bits = p.v_mode == TQ_MODE_INT8 ? 8 : p.v_bits;
+    a.qjl_dims = p.qjl_dims;
+    a.tok_per_tile = pl.tok_per_tile;
+    a.qtiles = pl.qtiles;
+    a.units = static_cast<int>(pl.units);
+    a.n_split = pl.n_split;
+    const double rd = std::sqrt(static_cast<double>(p.head_dim));
+    const double sm = p.sm_scale > 0.0f ? static_cast<double>(p.sm_scale) : 1.0 / rd;
+    // key centroids enter at the codebook's fp16 scale, which rounds the table
+    // best; the values' as sqrt(d)/4 c (times the largest fp16 norm they stay
+    // below the fp16 range)
+    const double ak = a.k_bits == 8 ? 1.0 : kcb->fp16_scale > 0.0 ? kcb->fp16_scale : rd;
+    a.key_scale = static_cast<float>(ak);
+    a.score_scale = static_cast<float>(sm * 1.4426950408889634 / ak);
+    a.out_scale = static_cast<float>(a.v_bits == 8 ? 1.0 : 4.0 / rd);
+    for (int j = 0; j < 16; ++j) {
+        a.kcent32[j] = a.k_bits < 8 && j < (1 << a.k_bits) ? static_cast<float>(kcb->centroids[j] * ak) : 0.f;
+        a.vcent32[j] = a.v_bits < 8 && j < (1 << a.v_bits) ? static_cast<float>(vcb->centroids[j] * rd * 0.25) : 0.f;
+    }
+    rotation_sign_bits(p.seed, p.head_dim, a.signs);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    switch (p.head_dim) {
+        case 64: e = launch_general<64>(a, s); break;
+        case 128: e = launch_general<128>(a, s); break;
+        default: e = launch_general<256>(a, s); break;
+    }
+    return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+}  // namespace tree
+}  // namespace tq
+
+// =================================================================== C ABI
+extern "C" {
+
+tq_status tq_tree_workspace_bytes(const tq_params* params, int32_t batch, int32_t n_draft, size_t* bytes) {
+    using namespace tq;
+    const tq_status st = validate_params(params);
+    if (st != TQ_OK) return st;
+    if (!bytes || batch < 1 || n_draft < 1) return TQ_ERR_INVALID_ARG;
+    if (n_draft > tree::MAX_DRAFTS) return TQ_ERR_UNSUPPORTED;
+    const int sms = num_sms_current();
+    if (sms <= 0) return TQ_ERR_CUDA;
+    *bytes = tree::general_plan(*params, batch, n_draft, sms).bytes;
+    return TQ_OK;
+}
+
+tq_status tq_tree_attention(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const void* d_q,
+                            tq_dtype q_dtype, int32_t n_draft, const uint64_t* d_mask, const int32_t* d_base_lens,
+                            const int32_t* d_draft_lens, const tq_cache* cache, void* d_out, tq_dtype out_dtype,
+                            void* d_workspace, size_t workspace_bytes, uint32_t* d_error, void* stream) {
+    return tq::tree::attend(params, kcb, vcb, d_q, q_dtype, n_draft, d_mask, d_base_lens, d_draft_lens, cache, nullptr,
+                            d_out, out_dtype, d_workspace, workspace_bytes, d_error, stream);
+}
+
+tq_status tq_tree_attention_paged(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb,
+                                  const void* d_q, tq_dtype q_dtype, int32_t n_draft, const uint64_t* d_mask,
+                                  const int32_t* d_base_lens, const int32_t* d_draft_lens, const tq_cache* pool,
+                                  const tq_block_table* table, void* d_out, tq_dtype out_dtype, void* d_workspace,
+                                  size_t workspace_bytes, uint32_t* d_error, void* stream) {
+    if (!params) return TQ_ERR_INVALID_ARG;
+    tq::PageMap pm;
+    const tq_status st = tq::validate_pages(*params, pool, table, &pm);
+    if (st != TQ_OK) return st;
+    return tq::tree::attend(params, kcb, vcb, d_q, q_dtype, n_draft, d_mask, d_base_lens, d_draft_lens, pool, &pm,
+                            d_out, out_dtype, d_workspace, workspace_bytes, d_error, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,201 @@
+// What the tree-attention kernels share: their arguments, the merge of
+// partial results, and the visibility rule.
+//
+// Query row (t, g) of unit (sequence b, kv head) is draft t with head g of
+// the kv head's group.  It sees the L = base[b] slots before the tree, and
+// slot L + j where bit j of mask[b][t] is set and j is below the sequence's
+// draft count.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "device_common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace tq {
+namespace tree {
+
+constexpr int MAX_DRAFTS = 64;  // bits of a mask word
+
+struct Args {
+    const uint8_t* k_codes;
+    const uint8_t* v_codes;
+    const uint16_t* k_norms;
+    const uint16_t* v_norms;
+    const uint8_t* k_qjl;
+    const uint16_t* k_gamma;
+    const float* sketch;
+    const void* q;               // [batch][n_draft][hq][d]
+    const uint64_t* mask;        // [batch][n_draft]
+    const int32_t* base;         // [batch] slots before the tree
+    const int32_t* draft_lens;   // [batch] or null: n_draft for all
+    void* out;                   // [batch][n_draft][hq][d]
+    uint32_t* err;
+    float* parts;                // partial results (see the kernels)
+    uint32_t* sched;             // [units + 1] (tensor-memory kernel)
+    const int32_t* table;        // paged, or null
+    int max_blocks, block_size, num_blocks;
+    int q_dtype, out_dtype, batch, hq, hkv, group, capacity, n_draft;
+    int k_bits, v_bits, qjl_dims;  // 8 bits: an int8 side
+    int staged_norms;              // rows of norms are 16-byte aligned every 8 slots
+    int tok_per_tile, qtiles, units, n_split, spread;
+    float score_scale, out_scale, key_scale;
+    uint32_t signs[8];
+    uint16_t kcent[16], vcent[16];  // fp16 centroids (tensor-memory kernel)
+    float kcent32[16], vcent32[16];
+};
+
+// A row's softmax reference before it has seen a key: below every score, but
+// finite, so that masked scores (-inf) weigh 2^-inf = 0 against it and a NaN
+// score stays NaN.
+constexpr float NOTHING = -1e30f;
+// What a piece leaves as its reference: -inf marks rows without a weight.
+__device__ __forceinline__ float piece_reference(float m, float l) { return m <= NOTHING && l == 0.f ? -INFINITY : m; }
+
+// One unit: a run of query rows of one (sequence, kv head).
+struct Unit {
+    int qt, kv, b, tok0, base, drafts, ntok, kend, ntiles;
+    bool bad;
+};
+
+template <int BK>
+__device__ __forceinline__ Unit unit_of(const Args& a, int u) {
+    Unit x;
+    x.qt = u % a.qtiles;
+    const int bk = u / a.qtiles;
+    x.kv = bk % a.hkv;
+    x.b = bk / a.hkv;
+    x.tok0 = x.qt * a.tok_per_tile;
+    x.base = a.base[x.b];
+    x.drafts = a.draft_lens ? a.draft_lens[x.b] : a.n_draft;
+    x.bad = x.drafts < 0 || x.drafts > a.n_draft || x.base < 0 || x.base > a.capacity - x.drafts;
+    x.ntok = x.bad ? 0 : max(0, min(a.tok_per_tile, x.drafts - x.tok0));
+    x.kend = x.ntok > 0 ? x.base + x.drafts : 0;
+    x.ntiles = (x.kend + BK - 1) / BK;
+    return x;
+}
+
+// Visible keys of a row among slots key0 .. key0 + 63, as bits: those before
+// `base`, and draft j = slot - base where bit j of m is set (m holds no bit
+// at or past the draft count).
+__device__ __forceinline__ uint64_t visible(uint64_t m, int key0, int base) {
+    const int before = base - key0;  // slots of the tile before the tree
+    if (before >= 64) return ~0ull;
+    if (before >= 0) return ((1ull << before) - 1ull) | (m << before);
+    return before > -64 ? m >> -before : 0ull;
+}
+
+__device__ __forceinline__ uint64_t row_mask(const Args& a, const Unit& x, int t) {
+    const uint64_t m = a.mask[static_cast<size_t>(x.b) * a.n_draft + t];
+    return x.drafts >= 64 ? m : m & ((1ull << x.drafts) - 1ull);
+}
+
+// Cache row (in units of one vector) of slot t of (b, kv).  An entry outside
+// the pool sets TQ_DEVERR_PAGE and block 0 is read in its place.
+__device__ __forceinline__ size_t cache_row(const Args& a, int b, int kv, int t) {
+    if (!a.table) return (static_cast<size_t>(b) * a.hkv + kv) * a.capacity + t;
+    int blk = a.table[static_cast<size_t>(b) * a.max_blocks + t / a.block_size];
+    if (blk < 0 || blk >= a.num_blocks) {
+        if (a.err) atomicOr(a.err, TQ_DEVERR_PAGE);
+        blk = 0;
+    }
+    return (static_cast<size_t>(blk) * a.hkv + kv) * a.block_size + t % a.block_size;
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int dtype) {
+    if (dtype == TQ_F16) return ptx::pack_half2(lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// N consecutive values (N = 2, 4 or 8) in any of the three output types.
+template <int N>
+__device__ __forceinline__ void store_row(void* base, size_t off, const float (&e)[N], int dtype) {
+    if (dtype == TQ_F32) {
+        float* p = static_cast<float*>(base) + off;
+#pragma unroll
+        for (int i = 0; i < N; i += 2) *reinterpret_cast<float2*>(p + i) = make_float2(e[i], e[i + 1]);
+    } else {
+        uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + off);
+        if constexpr (N == 2) {
+            *p = pack16(e[0], e[1], dtype);
+        } else if constexpr (N == 4) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack16(e[0], e[1], dtype), pack16(e[2], e[3], dtype));
+        } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(pack16(e[0], e[1], dtype), pack16(e[2], e[3], dtype),
+                                                      pack16(e[4], e[5], dtype), pack16(e[6], e[7], dtype));
+        }
+    }
+}
+
+// The output of one row from its partial results, by one warp (D / 32
+// channels a lane): piece j holds unnormalised O_j with the reference m_j
+// (log2 units) and the sum l_j;
+//   out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j,  M = max_j m_j,
+// then the inverse rotation (turbo values).  piece(j) gives a piece's rows
+// [ROWS][D], then [ROWS] m, then [ROWS] l.  A row that saw nothing is zero.
+constexpr int MERGE_BATCH = 16;
+template <int D, int ROWS, typename Piece>
+__device__ __forceinline__ void merge_row(const Args& a, Piece piece, int np, int r, size_t dst, bool store) {
+    constexpr int N = D / 32;
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    float M = -INFINITY;
+    for (int j = lane; j < np; j += 32) M = fmaxf(M, __ldcg(piece(j) + ROWS * D + r));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+    float L = 0.f, e[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = 0.f;
+    for (int j0 = 0; j0 < np; j0 += 32) {
+        float w = 0.f;  // the weight of piece j0 + lane
+        if (j0 + lane < np) {
+            const float* sp = piece(j0 + lane);
+            const float mk = __ldcg(sp + ROWS * D + r);
+            if (mk > -INFINITY) {
+                w = ptx::ex2(mk - M);
+                L = fmaf(__ldcg(sp + ROWS * D + ROWS + r), w, L);
+            }
+        }
+        const int nj = min(32, np - j0);
+        for (int b = 0; b < nj; b += MERGE_BATCH) {
+            float v[MERGE_BATCH][N], wk[MERGE_BATCH];
+#pragma unroll
+            for (int k = 0; k < MERGE_BATCH; ++k) {
+                wk[k] = __shfl_sync(kFullMask, w, (b + k) & 31);
+                if (b + k >= nj) wk[k] = 0.f;
+                // (an empty piece's rows were never written: they are not read)
+                const float* p = piece(j0 + (wk[k] != 0.f ? b + k : 0)) + r * D + lane * N;
+#pragma unroll
+                for (int i = 0; i < N; i += 2) {
+                    const float2 y = wk[k] != 0.f ? __ldcg(reinterpret_cast<const float2*>(p + i)) : make_float2(0.f, 0.f);
+                    v[k][i] = y.x;
+                    v[k][i + 1] = y.y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < MERGE_BATCH; ++k)
+#pragma unroll
+                for (int i = 0; i < N; ++i) e[i] = fmaf(v[k][i], wk[k], e[i]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(kFullMask, L, o);
+    const float inv = L == 0.f ? 0.f : a.out_scale / L;  // (NaN stays NaN)
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] *= inv;
+    if (a.v_bits != 8) {
+        fwht_registers(e);
+        fwht_lanes<N, 32>(e, lane);
+        const float rs = rsqrtf(static_cast<float>(D));
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = flip_sign(e[i] * rs, sign_bit(a.signs, lane * N + i));
+    }
+    if (store) store_row<N>(a.out, dst + lane * N, e, a.out_dtype);
+}
+
+}  // namespace tree
+}  // namespace tq

@@ -25,6 +25,9 @@ TQ_MODE_TURBO, TQ_MODE_INT8 = 0, 1
 TQ_F32, TQ_BF16, TQ_F16 = 0, 1, 2
 TQ_DEVERR_POSITION, TQ_DEVERR_SEQLEN, TQ_DEVERR_TIMEOUT, TQ_DEVERR_PAGE = 0x1, 0x2, 0x4, 0x8
 TQ_PARAM_PREFETCH_EARLY = 0x1
+TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
+TQ_ROPE_SCALE_NONE, TQ_ROPE_SCALE_LINEAR, TQ_ROPE_SCALE_BASE = 0, 1, 2
+TQ_ROPE_SCALE_WAVELENGTH, TQ_ROPE_SCALE_RAMP = 3, 4
 
 # every symbol include/tq.h declares
 EXPORTED = (
@@ -33,6 +36,8 @@ EXPORTED = (
     "tq_decode_attention", "tq_append_decode_attention", "tq_decode_attention_static", "tq_read_device_error",
     "tq_quantize_append_paged", "tq_decode_attention_paged", "tq_append_decode_attention_paged",
     "tq_prefill_attention", "tq_decode_static_fill", "tq_prefill_workspace_bytes",
+    "tq_rope_init", "tq_rope_append", "tq_rope_append_paged", "tq_tree_attention", "tq_tree_attention_paged",
+    "tq_tree_workspace_bytes", "tq_commit_drafts", "tq_commit_drafts_paged", "tq_read_back", "tq_read_back_paged",
 )
 
 # Bytes of the library's own decode scratch per device (tq_decode_attention_static).
@@ -71,6 +76,11 @@ class tq_cache(ctypes.Structure):
 
 class tq_block_table(ctypes.Structure):
     _fields_ = [("d_table", ctypes.c_void_p), ("batch", ctypes.c_int32), ("max_blocks", ctypes.c_int32)]
+
+
+class tq_rope(ctypes.Structure):
+    _fields_ = [("rotary_dims", ctypes.c_int32), ("layout", ctypes.c_int32), ("magnitude", ctypes.c_double),
+                ("turns", ctypes.c_uint64 * 128)]
 
 
 _P = ctypes.POINTER
@@ -119,6 +129,29 @@ _lib.tq_prefill_attention.argtypes = [_P(tq_params), _P(tq_codebook), _P(tq_code
                                       ctypes.c_void_p, _P(tq_cache), ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]
 _lib.tq_prefill_workspace_bytes.argtypes = [_P(tq_params), ctypes.c_int32, ctypes.c_int32, _P(ctypes.c_size_t)]
+_lib.tq_rope_init.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_double, ctypes.c_int32, ctypes.c_double,
+                              ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, _P(tq_rope)]
+_ROPE_APPEND = [_P(tq_params), _P(tq_codebook), _P(tq_codebook), _P(tq_rope), ctypes.c_void_p, ctypes.c_int64,
+                ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int32,
+                ctypes.c_void_p, ctypes.c_void_p, _P(tq_cache)]
+_lib.tq_rope_append.argtypes = _ROPE_APPEND + [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+_lib.tq_rope_append_paged.argtypes = _ROPE_APPEND + [_P(tq_block_table), ctypes.c_void_p, ctypes.c_void_p,
+                                                     ctypes.c_void_p]
+_TREE = [_P(tq_params), _P(tq_codebook), _P(tq_codebook), ctypes.c_void_p, ctypes.c_int, ctypes.c_int32,
+         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, _P(tq_cache)]
+_TREE_OUT = [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]
+_lib.tq_tree_attention.argtypes = _TREE + _TREE_OUT
+_lib.tq_tree_attention_paged.argtypes = _TREE + [_P(tq_block_table)] + _TREE_OUT
+_lib.tq_tree_workspace_bytes.argtypes = [_P(tq_params), ctypes.c_int32, ctypes.c_int32, _P(ctypes.c_size_t)]
+_COMMIT = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+           ctypes.c_void_p]
+_lib.tq_commit_drafts.argtypes = [ctypes.c_int32, _P(tq_params), _P(tq_cache)] + _COMMIT
+_lib.tq_commit_drafts_paged.argtypes = [ctypes.c_int32, _P(tq_params), _P(tq_cache), _P(tq_block_table)] + _COMMIT
+_READ = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+         ctypes.c_void_p, ctypes.c_void_p]
+_lib.tq_read_back.argtypes = [_P(tq_params), _P(tq_codebook), _P(tq_codebook), _P(tq_cache)] + _READ
+_lib.tq_read_back_paged.argtypes = [_P(tq_params), _P(tq_codebook), _P(tq_codebook), _P(tq_cache),
+                                    _P(tq_block_table)] + _READ
 for _name in EXPORTED:
     if _name not in ("tq_status_string", "tq_abi_version"):
         getattr(_lib, _name).restype = ctypes.c_int
@@ -387,6 +420,165 @@ def tq_append_decode_attention_paged(params, kcb, vcb, k_new, v_new, q, pool, ta
                                                _ptr(workspace), workspace.numel() * workspace.element_size(),
                                                _ptr(skip_mask), _ptr(error), _stream(stream))
     _check(st, "tq_append_decode_attention_paged")
+
+
+# ------------------------------------------------ drafted tokens, rotary positions
+def tq_rope_init(rotary_dims, layout=TQ_ROPE_HALF, base=10000.0, scaling=TQ_ROPE_SCALE_NONE, factor=1.0, low=1.0,
+                 high=4.0, trained_len=8192.0, magnitude=0.0):
+    """A layer's rotary table (see include/tq.h for the scalings)."""
+    rope = tq_rope()
+    _check(_lib.tq_rope_init(rotary_dims, layout, base, scaling, factor, low, high, trained_len, magnitude,
+                             ctypes.byref(rope)), "tq_rope_init")
+    return rope
+
+
+def _token_stride(t, name):
+    """Elements between tokens of t [batch, n, heads, d]: heads and channels contiguous, tokens evenly spaced over the
+    whole batch (a slice of a projection's output qualifies)."""
+    b, n, h, d = t.shape
+    row = t.stride(1) if n > 1 else t.stride(0) if b > 1 else h * d
+    if (row < h * d or (d > 1 and t.stride(3) != 1) or (h > 1 and t.stride(2) != d)
+            or (b > 1 and n > 1 and t.stride(0) != n * row)):
+        raise ValueError("%s: heads and channels must be contiguous and tokens evenly spaced" % name)
+    return row
+
+
+def _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, q_out, rope_positions):
+    assert k_new.dtype == v_new.dtype and k_new.shape == v_new.shape and k_new.shape[2] == params.num_kv_heads
+    assert k_new.shape[3] == params.head_dim and positions.dtype == torch.int32 and positions.is_cuda
+    assert positions.is_contiguous() and positions.numel() == k_new.shape[0]
+    assert (q is None) == (q_out is None)
+    stride = 0
+    if q is not None:
+        assert q.dtype == k_new.dtype and q_out.dtype == q.dtype and q_out.shape == q.shape and q_out.is_contiguous()
+        assert q.shape == k_new.shape[:2] + (params.num_q_heads, params.head_dim)
+        stride = _token_stride(q, "q")
+    if rope_positions is not None:
+        assert rope_positions.dtype == torch.int32 and rope_positions.is_cuda and rope_positions.is_contiguous()
+        assert rope_positions.shape == k_new.shape[:2]
+    return (ctypes.byref(params), kcb and ctypes.byref(kcb), vcb and ctypes.byref(vcb), ctypes.byref(rope), _ptr(q),
+            stride, _ptr(k_new), _token_stride(k_new, "k_new"), _ptr(v_new), _token_stride(v_new, "v_new"),
+            _dtype_code(k_new), k_new.shape[1], _ptr(positions), _ptr(rope_positions), ctypes.byref(cache.struct()))
+
+
+def tq_rope_append(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, q_out, rope_positions=None, error=None,
+                   stream=None):
+    """Turn q ([batch, n_new, Hq, d]) into q_out and append k_new (turned) and v_new ([batch, n_new, Hkv, d]) at slots
+    positions[b] ..; rope_positions: int32 [batch, n_new] or None (the slots).  q, k_new and v_new may be slices of one
+    projection's output; q and q_out may be None, or the same tensor."""
+    assert positions.numel() == cache.batch
+    args = _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, q_out, rope_positions)
+    _check(_lib.tq_rope_append(*args, _ptr(q_out), _ptr(error), _stream(stream)), "tq_rope_append")
+
+
+def tq_rope_append_paged(params, kcb, vcb, rope, q, k_new, v_new, positions, pool, table, q_out, rope_positions=None,
+                         error=None, stream=None):
+    """tq_rope_append on a paged cache (see tq_quantize_append_paged)."""
+    bt = block_table(table)
+    assert positions.numel() == bt.batch
+    args = _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, pool, q_out, rope_positions)
+    _check(_lib.tq_rope_append_paged(*args, ctypes.byref(bt), _ptr(q_out), _ptr(error), _stream(stream)),
+           "tq_rope_append_paged")
+
+
+def tq_tree_workspace_bytes(params, batch, n_draft):
+    n = ctypes.c_size_t(0)
+    _check(_lib.tq_tree_workspace_bytes(ctypes.byref(params), batch, n_draft, ctypes.byref(n)),
+           "tq_tree_workspace_bytes")
+    return int(n.value)
+
+
+def _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, cache, batch, out):
+    assert q.is_contiguous() and out.is_contiguous() and out.shape == q.shape
+    assert q.shape[0] == batch and q.shape[2] == params.num_q_heads and q.shape[3] == params.head_dim
+    assert tree_mask.dtype == torch.int64 and tree_mask.is_cuda and tree_mask.is_contiguous()
+    assert tree_mask.shape == q.shape[:2]
+    for t in (base_lens, draft_lens):
+        assert t is None or (t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == batch)
+    return (ctypes.byref(params), kcb and ctypes.byref(kcb), vcb and ctypes.byref(vcb), _ptr(q), _dtype_code(q),
+            q.shape[1], _ptr(tree_mask), _ptr(base_lens), _ptr(draft_lens), ctypes.byref(cache.struct()))
+
+
+def tq_tree_attention(params, kcb, vcb, q, tree_mask, base_lens, cache, out, workspace, draft_lens=None, error=None,
+                      stream=None):
+    """Attention of drafted tokens: q [batch, n_draft, Hq, d] over the base_lens[b] slots before the tree and, of the
+    drafts in the slots after them, those whose bits tree_mask (int64 [batch, n_draft]) has set; out: like q, in fp32,
+    bf16 or fp16.  workspace: uint8, tq_tree_workspace_bytes(params, batch, n_draft), any contents."""
+    args = _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, cache, cache.batch, out)
+    _check(_lib.tq_tree_attention(*args, _ptr(out), _dtype_code(out), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _ptr(error), _stream(stream)),
+           "tq_tree_attention")
+
+
+def tq_tree_attention_paged(params, kcb, vcb, q, tree_mask, base_lens, pool, table, out, workspace, draft_lens=None,
+                            error=None, stream=None):
+    """tq_tree_attention on a paged cache (see tq_quantize_append_paged)."""
+    bt = block_table(table)
+    args = _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, pool, bt.batch, out)
+    _check(_lib.tq_tree_attention_paged(*args, ctypes.byref(bt), _ptr(out), _dtype_code(out), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _ptr(error), _stream(stream)),
+           "tq_tree_attention_paged")
+
+
+class draft_layers:
+    """The layers a commit moves drafts in, kept by the program between steps: [(params, CacheTensors), ...]."""
+
+    def __init__(self, layers):
+        self.layers = list(layers)  # (keeps the tensors alive)
+        n = len(self.layers)
+        self.params = (tq_params * n)(*[p for p, _ in self.layers])
+        self.caches = (tq_cache * n)(*[c.struct() for _, c in self.layers])
+
+
+def _commit_call(path, path_lens, base_lens, new_lens, batch):
+    assert path.dtype == torch.int32 and path.is_cuda and path.is_contiguous() and path.dim() == 2
+    assert path.shape[0] == batch
+    for t in (path_lens, base_lens, new_lens):
+        assert t is None or (t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == batch)
+    return _ptr(path), path.shape[1], _ptr(path_lens), _ptr(base_lens), _ptr(new_lens)
+
+
+def tq_commit_drafts(layers, path, path_lens, base_lens, new_lens=None, error=None, stream=None):
+    """Move draft path[b, i] (int32 [batch, max_path]) to slot base_lens[b] + i, i < path_lens[b], in every layer of a
+    draft_layers; new_lens: base_lens + path_lens."""
+    args = _commit_call(path, path_lens, base_lens, new_lens, layers.caches[0].batch if len(layers.layers) else 0)
+    _check(_lib.tq_commit_drafts(len(layers.layers), layers.params, layers.caches, *args, _ptr(error),
+                                 _stream(stream)), "tq_commit_drafts")
+
+
+def tq_commit_drafts_paged(layers, table, path, path_lens, base_lens, new_lens=None, error=None, stream=None):
+    """tq_commit_drafts on paged caches that share one block table."""
+    bt = block_table(table)
+    args = _commit_call(path, path_lens, base_lens, new_lens, bt.batch)
+    _check(_lib.tq_commit_drafts_paged(len(layers.layers), layers.params, layers.caches, ctypes.byref(bt), *args,
+                                       _ptr(error), _stream(stream)), "tq_commit_drafts_paged")
+
+
+def _read_call(params, starts, counts, batch, k_out, v_out):
+    outs = [t for t in (k_out, v_out) if t is not None]
+    assert outs and all(t.is_contiguous() and t.dtype == outs[0].dtype and t.shape == outs[0].shape for t in outs)
+    assert outs[0].shape[0] == batch and outs[0].shape[2:] == (params.num_kv_heads, params.head_dim)
+    for t in (starts, counts):
+        assert t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == batch
+    return _ptr(starts), _ptr(counts), outs[0].shape[1], _dtype_code(outs[0]), _ptr(k_out), _ptr(v_out)
+
+
+def tq_read_back(params, kcb, vcb, cache, starts, counts, k_out=None, v_out=None, error=None, stream=None):
+    """Reconstruct slots starts[b] .. starts[b] + counts[b] - 1 of every sequence into k_out and v_out
+    ([batch, max_count, Hkv, d], fp32, bf16 or fp16); rows past counts[b] are left as they are."""
+    args = _read_call(params, starts, counts, cache.batch, k_out, v_out)
+    _check(_lib.tq_read_back(ctypes.byref(params), kcb and ctypes.byref(kcb), vcb and ctypes.byref(vcb),
+                             ctypes.byref(cache.struct()), *args, _ptr(error), _stream(stream)), "tq_read_back")
+
+
+def tq_read_back_paged(params, kcb, vcb, pool, table, starts, counts, k_out=None, v_out=None, error=None,
+                       stream=None):
+    """tq_read_back on a paged cache (see tq_quantize_append_paged)."""
+    bt = block_table(table)
+    args = _read_call(params, starts, counts, bt.batch, k_out, v_out)
+    _check(_lib.tq_read_back_paged(ctypes.byref(params), kcb and ctypes.byref(kcb), vcb and ctypes.byref(vcb),
+                                   ctypes.byref(pool.struct()), ctypes.byref(bt), *args, _ptr(error),
+                                   _stream(stream)), "tq_read_back_paged")
 
 
 def tq_read_device_error(error, stream=None, timeout_ms=2000):

@@ -486,6 +486,166 @@ tq_status tq_decode_static_fill(uint8_t value, void* stream);
  */
 tq_status tq_read_device_error(const uint32_t* d_error, uint32_t* out, void* stream, int32_t timeout_ms);
 
+/*
+ * Rotary positions.  The pages say nothing of positions; these calls follow
+ * the usual definition: pair i of the first rotary_dims coordinates of a head
+ * is turned by the angle position * f_i and scaled by a magnitude g,
+ *     (a, b) -> g (a cos - b sin, b cos + a sin),
+ * the other coordinates pass through.  Layouts: pairs (i, i + r/2) or
+ * (2i, 2i + 1), r = rotary_dims.
+ */
+typedef enum tq_rope_layout { TQ_ROPE_HALF = 0, TQ_ROPE_INTERLEAVED = 1 } tq_rope_layout;
+
+/*
+ * Scaling of the frequencies f_i = base^(-2i/r) for contexts longer than the
+ * trained one, by `factor`:
+ *   LINEAR      f / factor
+ *   BASE        base * factor^(r/(r-2)) in place of base
+ *   WAVELENGTH  with s = clamp((T - low) / (high - low), 0, 1), T = trained_len f / 2 pi
+ *               the turns within the trained length: (1 - s) f / factor + s f
+ *   RAMP        s = clamp((i - i0) / (i1 - i0), 0, 1) over the pairs:
+ *               s f / factor + (1 - s) f, with i0 = max(0, floor(at(high))),
+ *               i1 = min(r - 1, ceil(at(low))), at(n) = r ln(trained_len / 2 pi n) / (2 ln base)
+ *               (i1 - i0 at least 0.001)
+ */
+typedef enum tq_rope_scaling {
+    TQ_ROPE_SCALE_NONE = 0,
+    TQ_ROPE_SCALE_LINEAR = 1,
+    TQ_ROPE_SCALE_BASE = 2,
+    TQ_ROPE_SCALE_WAVELENGTH = 3,
+    TQ_ROPE_SCALE_RAMP = 4
+} tq_rope_scaling;
+
+/* A layer's rotary table: plain data, owned by the caller. */
+typedef struct tq_rope {
+    int32_t rotary_dims;
+    int32_t layout;
+    double magnitude;    /* g */
+    uint64_t turns[128]; /* turns per position of pair i, modulo one, in 2^-64ths */
+} tq_rope;
+
+/*
+ * Host only.  Fill *out.  rotary_dims: even, 2 .. 256; base > 1; low, high,
+ * trained_len are read by WAVELENGTH and RAMP (0 < low < high), factor > 0 by
+ * every scaling.  magnitude 0 selects 1, or with RAMP max(1, 0.1 ln(factor) + 1).
+ */
+tq_status tq_rope_init(int32_t rotary_dims, int32_t layout, double base, int32_t scaling, double factor, double low,
+                       double high, double trained_len, double magnitude, tq_rope* out);
+
+/*
+ * Rotary positions and append in one kernel: the queries are turned into
+ * q_out, the keys turned and quantised, the values quantised, and both
+ * appended as tq_quantize_append does (the turned key stays in fp32 until its
+ * norm and codes are taken).
+ *   q, k_new, v_new  device, `dtype`: batch * n_new tokens, *_stride elements
+ *                    apart (0: contiguous), [heads][d] each, so that slices
+ *                    of one projection's output need no copy.  16-byte
+ *                    aligned, strides multiples of 16 bytes.  q and q_out
+ *                    may both be NULL.
+ *   d_positions      device int32 [batch]: the first slot, as tq_quantize_append.
+ *   d_rope_positions device int32 [batch][n_new]: the position each token is
+ *                    turned by (a tree's drafts repeat depths), any int32; or
+ *                    NULL: its slot.
+ *   q_out            device, [batch][n_new][Hq][d] in `dtype`; may be q when
+ *                    that is contiguous, else must not overlap the inputs.
+ * A sequence whose slots are out of range gets no append and sets
+ * TQ_DEVERR_POSITION; its queries are turned all the same.
+ */
+tq_status tq_rope_append(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const tq_rope* rope,
+                         const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                         int64_t v_stride, tq_dtype dtype, int32_t n_new, const int32_t* d_positions,
+                         const int32_t* d_rope_positions, const tq_cache* cache, void* q_out, uint32_t* d_error,
+                         void* stream);
+tq_status tq_rope_append_paged(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb,
+                               const tq_rope* rope, const void* q, int64_t q_stride, const void* k_new,
+                               int64_t k_stride, const void* v_new, int64_t v_stride, tq_dtype dtype, int32_t n_new,
+                               const int32_t* d_positions, const int32_t* d_rope_positions, const tq_cache* pool,
+                               const tq_block_table* table, void* q_out, uint32_t* d_error, void* stream);
+
+/*
+ * Attention of a tree of drafted tokens over the cache (speculative
+ * decoding).  The drafts' keys and values were appended to slots
+ * base_lens[b] .. base_lens[b] + drafts - 1; draft t of sequence b attends to
+ * the base_lens[b] slots before the tree, and to draft j where bit j of
+ * d_mask[b][t] is set (its ancestors and itself), as a decode step over those
+ * slots would.  A draft that sees nothing gets zeros.
+ *   d_q           device, [batch][n_draft][Hq][d] in q_dtype.
+ *   n_draft       1 .. 64 (more: TQ_ERR_UNSUPPORTED).
+ *   d_mask        device uint64 [batch][n_draft]; bits at or past the
+ *                 sequence's draft count are ignored.
+ *   d_base_lens   device int32 [batch], 0 or more.
+ *   d_draft_lens  device int32 [batch], drafts of each sequence (0 .. n_draft),
+ *                 or NULL: n_draft for all.  Output rows of a sequence past
+ *                 its drafts are left as they are.
+ *   d_out         device, [batch][n_draft][Hq][d] in out_dtype.
+ *   d_workspace   device scratch of tq_tree_workspace_bytes(params, batch,
+ *                 n_draft) bytes on the current device, 16-byte aligned, any
+ *                 contents.  Calls that overlap on the device need one each.
+ * A sequence with base_lens or draft_lens out of range (base_lens[b] + drafts
+ * above the capacity) sets TQ_DEVERR_SEQLEN and yields zeros.  A block-table
+ * entry outside the pool sets TQ_DEVERR_PAGE; that sequence's output is not
+ * valid.  sparse_v_threshold is not applied.  Every configuration of
+ * tq_params is taken; outputs are within 2e-3 (relative L2 per row) of exact
+ * attention over the stored codes, plus the rounding to out_dtype.
+ */
+tq_status tq_tree_attention(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const void* d_q,
+                            tq_dtype q_dtype, int32_t n_draft, const uint64_t* d_mask, const int32_t* d_base_lens,
+                            const int32_t* d_draft_lens, const tq_cache* cache, void* d_out, tq_dtype out_dtype,
+                            void* d_workspace, size_t workspace_bytes, uint32_t* d_error, void* stream);
+tq_status tq_tree_attention_paged(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb,
+                                  const void* d_q, tq_dtype q_dtype, int32_t n_draft, const uint64_t* d_mask,
+                                  const int32_t* d_base_lens, const int32_t* d_draft_lens, const tq_cache* pool,
+                                  const tq_block_table* table, void* d_out, tq_dtype out_dtype, void* d_workspace,
+                                  size_t workspace_bytes, uint32_t* d_error, void* stream);
+tq_status tq_tree_workspace_bytes(const tq_params* params, int32_t batch, int32_t n_draft, size_t* bytes);
+
+/*
+ * Commit the accepted path of a tree in every layer: draft path[b][i] (slot
+ * base_lens[b] + path[b][i]) moves to slot base_lens[b] + i, for
+ * i < path_lens[b], byte for byte; every row is read before any is written,
+ * so the path may name the drafts in any order.  Slots past the path keep
+ * what they held.
+ *   n_layers      layers; params and caches are host arrays of that length.
+ *                 The layers may differ in heads, widths and modes, not in
+ *                 batch or capacity.
+ *   d_path        device int32 [batch][max_path], draft indices 0 .. 63.
+ *   max_path      1 .. 64.
+ *   d_path_lens   device int32 [batch], 0 .. max_path.
+ *   d_base_lens   device int32 [batch], slots before the tree.
+ *   d_new_lens    device int32 [batch] or NULL: base_lens[b] + path_lens[b];
+ *                 must not overlap the other arrays.
+ * A sequence with an index, length or slot out of range moves nothing, keeps
+ * its base length and sets TQ_DEVERR_POSITION (TQ_DEVERR_PAGE for a
+ * block-table entry outside the pool).
+ */
+tq_status tq_commit_drafts(int32_t n_layers, const tq_params* params, const tq_cache* caches, const int32_t* d_path,
+                           int32_t max_path, const int32_t* d_path_lens, const int32_t* d_base_lens,
+                           int32_t* d_new_lens, uint32_t* d_error, void* stream);
+/* The layers' pools share one block table. */
+tq_status tq_commit_drafts_paged(int32_t n_layers, const tq_params* params, const tq_cache* pools,
+                                 const tq_block_table* table, const int32_t* d_path, int32_t max_path,
+                                 const int32_t* d_path_lens, const int32_t* d_base_lens, int32_t* d_new_lens,
+                                 uint32_t* d_error, void* stream);
+
+/*
+ * Reconstruct a range of slots of every sequence, as tq_dequantize does one
+ * sequence's: slots starts[b] .. starts[b] + counts[b] - 1 of sequence b.
+ *   d_starts, d_counts  device int32 [batch]; counts 0 .. max_count.
+ *   max_count           host bound on the counts; rows of the outputs.
+ *   d_k_out, d_v_out    device, [batch][max_count][Hkv][d] in out_dtype,
+ *                       16-byte aligned (either may be NULL); rows past
+ *                       counts[b] are left as they are.
+ * A range outside the cache is left alone and sets TQ_DEVERR_POSITION; rows
+ * behind a block-table entry outside the pool likewise, TQ_DEVERR_PAGE.
+ */
+tq_status tq_read_back(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const tq_cache* cache,
+                       const int32_t* d_starts, const int32_t* d_counts, int32_t max_count, tq_dtype out_dtype,
+                       void* d_k_out, void* d_v_out, uint32_t* d_error, void* stream);
+tq_status tq_read_back_paged(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb,
+                             const tq_cache* pool, const tq_block_table* table, const int32_t* d_starts,
+                             const int32_t* d_counts, int32_t max_count, tq_dtype out_dtype, void* d_k_out,
+                             void* d_v_out, uint32_t* d_error, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
