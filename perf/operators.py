@@ -283,6 +283,14 @@ def _paged(case, slots, g):
     return case["batch"] * blocks + 3, case["page"], order.view(case["batch"], blocks).to(torch.int32)
 
 
+@functools.lru_cache(maxsize=None)
+def _book(d, bits):
+    """A codebook of the library: a program makes it once, for all its layers and inputs."""
+    from bit_kv_cache_tq_b200 import tq
+
+    return tq.tq_codebook_init(d, bits)
+
+
 def _handles(case, cache, table):
     """What a user's program keeps of the library's: parameters, codebooks, the cache and the error word."""
     from bit_kv_cache_tq_b200 import tq
@@ -291,7 +299,7 @@ def _handles(case, cache, table):
     bits = [4 if b == 8 else b for b in (case["kb"], case["vb"])]
     p = tq.make_params(case["d"], case.get("hq", case["hkv"]), case["hkv"], bits[0], bits[1], modes[0], modes[1],
                        case["qjl"], SIGN_SEED)
-    books = [tq.tq_codebook_init(case["d"], b) if b < 8 else None for b in (case["kb"], case["vb"])]
+    books = [_book(case["d"], b) if b < 8 else None for b in (case["kb"], case["vb"])]
     return {"tq": tq, "p": p, "kcb": books[0], "vcb": books[1], "table": table,
             "err": torch.zeros(1, dtype=torch.int32, device="cuda")}
 
