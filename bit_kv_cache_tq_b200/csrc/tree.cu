@@ -1,5 +1,6 @@
 // Attention of a tree of drafted tokens over the cache: the general kernel,
-// and the C entry points.
+// the merge kernels and the C entry points (the tensor-memory kernel, which
+// d = 128 layers without a sketch take, is in tree_mma_impl.cuh).
 //
 // For draft t of sequence b and query head h (kv head h / (Hq / Hkv)):
 //   s_i = sm_scale <q, k_hat_i>,  p = softmax over the slots the draft sees,
@@ -19,6 +20,7 @@
 // merge kernel joins the pieces.
 
 #include "tree_common.cuh"
+#include "tree_mma_impl.cuh"
 
 namespace tq {
 namespace tree {
@@ -314,11 +316,54 @@ __global__ void __launch_bounds__(MERGE_THREADS) tree_general_merge_kernel(const
         true);
 }
 
+// The rows of the units that the tensor-memory kernel cut between blocks
+// (it wrote the others' outputs itself), one warp per row.
+__global__ void __launch_bounds__(MERGE_THREADS) tree_mma_merge_kernel(const __grid_constant__ Args a, int nblocks) {
+    ptx::wait_prerequisites();  // launched as a programmatic dependent of the attention kernel
+    ptx::launch_dependents();
+    const int u = static_cast<int>(blockIdx.x);
+    const uint32_t total = a.sched[a.units], pu = a.sched[u], pn = a.sched[u + 1];
+    if (pn <= pu) return;
+    const uint32_t C = static_cast<uint32_t>(nblocks) > total ? total : static_cast<uint32_t>(nblocks);
+    const int ca = mma::block_of(pu, total, C), cz = mma::block_of(pn - 1, total, C);
+    if (ca == cz) return;
+    const Unit x = unit_of<mma::BK>(a, u);
+    const int r = static_cast<int>(blockIdx.y) * (MERGE_THREADS / 32) + (static_cast<int>(threadIdx.x) >> 5);
+    const int G = a.group, t = r / G, g = r % G;
+    if (t >= x.ntok) return;
+    const size_t dst = ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + t) * a.hq + x.kv * G + g) * mma::D;
+    merge_row<mma::D, mma::BM>(
+        a, [&](int j) { return a.parts + static_cast<size_t>(mma::part_slot(ca + j, ca)) * mma::PART_FLOATS; },
+        cz - ca + 1, r, dst, true);
+}
+
+// Work layout of a call.  general: n_split blocks per unit of GEN_ROWS rows.
+// Tensor-memory kernel: units of up to 128 rows (a sequence's drafts spread
+// evenly over its units), the tile sequence shared by one block per SM
+// (spread) or, past SCHED_MAX units, a block per unit; workspace: the schedule,
+// then two partial outputs per block.
 struct Plan {
     long long units;
-    int tok_per_tile, qtiles, n_split;
-    size_t bytes;
+    int tok_per_tile, qtiles, n_split, spread, blocks;
+    size_t sched_bytes, bytes;
 };
+
+static bool mma_supported(const tq_params& p) { return p.head_dim == mma::D && p.qjl_dims == 0; }
+
+static Plan mma_plan(const tq_params& p, int batch, int n_draft, int sms) {
+    Plan pl{};
+    const int most = mma::BM / (p.num_q_heads / p.num_kv_heads);
+    pl.qtiles = (n_draft + most - 1) / most;
+    pl.tok_per_tile = (n_draft + pl.qtiles - 1) / pl.qtiles;
+    pl.units = static_cast<long long>(batch) * p.num_kv_heads * pl.qtiles;
+    pl.spread = pl.units <= mma::SCHED_MAX;
+    pl.blocks = pl.spread ? sms : static_cast<int>(pl.units);
+    if (pl.spread) {
+        pl.sched_bytes = (static_cast<size_t>(pl.units + 1) * 4 + 255) / 256 * 256;
+        pl.bytes = pl.sched_bytes + 2ull * pl.blocks * mma::PART_FLOATS * sizeof(float);
+    }
+    return pl;
+}
 
 static Plan general_plan(const tq_params& p, int batch, int n_draft, int sms) {
     Plan pl{};
@@ -344,6 +389,24 @@ static cudaError_t launch_general(const Args& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+static cudaError_t launch_mma(const Args& a, const Plan& pl, cudaStream_t s) {
+    cudaError_t e;
+    switch (a.k_bits) {
+        case 2: e = launch_mma_k2(a.v_bits, a, pl.blocks, s); break;
+        case 3: e = launch_mma_k3(a.v_bits, a, pl.blocks, s); break;
+        case 4: e = launch_mma_k4(a.v_bits, a, pl.blocks, s); break;
+        default: e = launch_mma_k8(a.v_bits, a, pl.blocks, s); break;
+    }
+    if (e != cudaSuccess || !pl.spread) return e;
+    const int rows = (a.tok_per_tile * a.group + MERGE_THREADS / 32 - 1) / (MERGE_THREADS / 32);
+    return mma::launch_dependent(tree_mma_merge_kernel, dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(rows)),
+                                 dim3(MERGE_THREADS), 0u, s, a, pl.blocks);
+}
+
+static Plan plan_of(const tq_params& p, int batch, int n_draft, int sms) {
+    return mma_supported(p) ? mma_plan(p, batch, n_draft, sms) : general_plan(p, batch, n_draft, sms);
+}
+
 static tq_status attend(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const void* d_q,
                         tq_dtype q_dtype, int32_t n_draft, const uint64_t* d_mask, const int32_t* d_base,
                         const int32_t* d_draft_lens, const tq_cache* cache, const PageMap* pm, void* d_out,
@@ -363,11 +426,29 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     const int batch = pm ? pm->batch : cache->batch;
     const int sms = num_sms_current();
     if (sms <= 0) return TQ_ERR_CUDA;
-    const Plan pl = general_plan(p, batch, n_draft, sms);
+    const int capacity = pm ? pm->max_blocks * pm->block_size : cache->capacity;
+    const bool mm = mma_supported(p);
+    Plan pl = plan_of(p, batch, n_draft, sms);
     if (pl.units > INT32_MAX) return TQ_ERR_INVALID_ARG;
-    if (!d_workspace) return TQ_ERR_INVALID_ARG;
-    if (workspace_bytes < pl.bytes) return TQ_ERR_CAPACITY;
-    if (!aligned16(d_workspace)) return TQ_ERR_ALIGNMENT;
+    if (mm && pl.spread && pl.units * ((capacity + mma::BK - 1) / mma::BK) >= (1ll << 31)) {
+        // the shared tile sequence is counted in 32 bits: a block per unit instead
+        pl.spread = 0;
+        pl.blocks = static_cast<int>(pl.units);
+        pl.bytes = 0;
+    }
+    if (pl.bytes > 0) {
+        if (!d_workspace) return TQ_ERR_INVALID_ARG;
+        if (workspace_bytes < pl.bytes) return TQ_ERR_CAPACITY;
+        if (!aligned16(d_workspace)) return TQ_ERR_ALIGNMENT;
+    }
+    if (mm && mma::wide(p.k_mode == TQ_MODE_INT8 ? 8 : p.k_bits)) {
+        // the 4-bit key table's lookups carry its shared-window address
+        int reserved = 0, dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess)
+            return TQ_ERR_CUDA;
+        if (static_cast<uint32_t>(reserved) != mma::SMEM_WINDOW) return TQ_ERR_UNSUPPORTED;
+    }
     Args a{};
     a.k_codes = cache->k_codes;
     a.v_codes = cache->v_codes;
@@ -382,8 +463,9 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     a.draft_lens = d_draft_lens;
     a.out = d_out;
     a.err = d_error;
-    a.parts = static_cast<float*>(d_workspace);
-    a.capacity = pm ? pm->max_blocks * pm->block_size : cache->capacity;
+    a.sched = static_cast<uint32_t*>(d_workspace);
+    a.parts = reinterpret_cast<float*>(static_cast<char*>(d_workspace) + pl.sched_bytes);
+    a.capacity = capacity;
     if (pm) {
         a.table = pm->table;
         a.max_blocks = pm->max_blocks;
@@ -404,6 +486,8 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     a.qtiles = pl.qtiles;
     a.units = static_cast<int>(pl.units);
     a.n_split = pl.n_split;
+    a.spread = pl.spread;
+    a.staged_norms = pm || capacity % 8 == 0;
     const double rd = std::sqrt(static_cast<double>(p.head_dim));
     const double sm = p.sm_scale > 0.0f ? static_cast<double>(p.sm_scale) : 1.0 / rd;
     // key centroids enter at the codebook's fp16 scale, which rounds the table
@@ -412,15 +496,20 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     const double ak = a.k_bits == 8 ? 1.0 : kcb->fp16_scale > 0.0 ? kcb->fp16_scale : rd;
     a.key_scale = static_cast<float>(ak);
     a.score_scale = static_cast<float>(sm * 1.4426950408889634 / ak);
-    a.out_scale = static_cast<float>(a.v_bits == 8 ? 1.0 : 4.0 / rd);
+    // (the tensor-memory kernel rounds the value table itself to fp16: at its codebook's scale too)
+    const double av = a.v_bits == 8 ? 1.0 : 0.25 * (mm && vcb->fp16_scale > 0.0 ? vcb->fp16_scale : rd);
+    a.out_scale = static_cast<float>(1.0 / av);
     for (int j = 0; j < 16; ++j) {
         a.kcent32[j] = a.k_bits < 8 && j < (1 << a.k_bits) ? static_cast<float>(kcb->centroids[j] * ak) : 0.f;
-        a.vcent32[j] = a.v_bits < 8 && j < (1 << a.v_bits) ? static_cast<float>(vcb->centroids[j] * rd * 0.25) : 0.f;
+        a.vcent32[j] = a.v_bits < 8 && j < (1 << a.v_bits) ? static_cast<float>(vcb->centroids[j] * av) : 0.f;
+        a.kcent[j] = __half_as_ushort(__float2half_rn(a.kcent32[j]));
+        a.vcent[j] = __half_as_ushort(__float2half_rn(a.vcent32[j]));
     }
     rotation_sign_bits(p.seed, p.head_dim, a.signs);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    switch (p.head_dim) {
+    if (mm) e = launch_mma(a, pl, s);
+    else switch (p.head_dim) {
         case 64: e = launch_general<64>(a, s); break;
         case 128: e = launch_general<128>(a, s); break;
         default: e = launch_general<256>(a, s); break;
@@ -442,7 +531,7 @@ tq_status tq_tree_workspace_bytes(const tq_params* params, int32_t batch, int32_
     if (n_draft > tree::MAX_DRAFTS) return TQ_ERR_UNSUPPORTED;
     const int sms = num_sms_current();
     if (sms <= 0) return TQ_ERR_CUDA;
-    *bytes = tree::general_plan(*params, batch, n_draft, sms).bytes;
+    *bytes = tree::plan_of(*params, batch, n_draft, sms).bytes;
     return TQ_OK;
 }
 

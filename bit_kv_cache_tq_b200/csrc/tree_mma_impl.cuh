@@ -1,0 +1,853 @@
+// Tree attention on the 5th-generation tensor cores: d = 128, turbo or int8
+// keys and values without a sketch.
+//
+// The work is a sequence of key tiles (64 slots) of units (sequence, kv head,
+// up to 128 query rows); every block takes an equal run of it, so a unit may
+// be cut between blocks, whose pieces the merge kernel joins.
+//
+// A block's tiles alternate between two streams of online softmax over the
+// same query rows, each with its own scores, reference, sum and output
+// accumulator in tensor memory: while one stream's softmax runs, the tensor
+// cores work for the other.  The two are joined at the end of a unit's run,
+// where a row's two accumulators lie in the same tensor-memory lane.
+//
+// Roles (20 warps):
+//  * producer (1 warp): bulk copies of packed codes and norms into a ring;
+//  * dequantisers (8 warps): codes to fp16 operand tiles (128-byte swizzle),
+//    keys as centroids, values as centroids times norms;
+//  * MMA issuer (1 warp): S = (Qhi + Qlo) K~^T (M = 128, N = 64, K = 128) and
+//    O += P V~ (M = 128, N = 128, K = 64), the queries and the weights as A
+//    operands in tensor memory;
+//  * softmax (2 x 4 warps, one query row a thread): scores times key norms,
+//    the tree's mask, lazy online softmax, weights written over the scores.
+//
+// Every mbarrier wait is bounded (about a second, then TQ_DEVERR_TIMEOUT; the
+// block stops issuing, waits for its copies and MMAs, frees tensor memory).
+#pragma once
+
+#include "tcgen05.cuh"
+#include "tree_common.cuh"
+
+namespace tq {
+namespace tree {
+namespace mma {
+
+constexpr int D = 128, BM = 128, BK = 64, NS = 4;
+constexpr int SOFTMAX_WARPS = 8, DEQ_WARPS = 8;
+constexpr int DEQ0 = SOFTMAX_WARPS * 32, LIGHT0 = DEQ0 + DEQ_WARPS * 32;
+constexpr int PRODUCER_WARP = LIGHT0 / 32, MMA_WARP = PRODUCER_WARP + 1;
+constexpr int NTHREADS = LIGHT0 + 128;  // (two idle warps complete the last warpgroup)
+// Registers a thread: launched at 96, the last warpgroup and the
+// dequantisers give up what the softmax warpgroups take:
+// 256 x 152 + 256 x 64 + 128 x 40 <= 640 x 96.
+constexpr int REGS_LAUNCH = 96, REGS_SOFTMAX = 152, REGS_DEQ = 64, REGS_LIGHT = 40;
+static_assert(SOFTMAX_WARPS * 32 * REGS_SOFTMAX + DEQ_WARPS * 32 * REGS_DEQ + 128 * REGS_LIGHT <=
+                  NTHREADS * REGS_LAUNCH,
+              "the register split draws on what the block was launched with");
+// tensor-memory columns (32-bit; fp16 operands take two elements a column)
+constexpr uint32_t TM_QHI = 0, TM_QLO = 64;  // queries / row scale, fp16 [128][128], and their remainder
+constexpr uint32_t TM_S = 128;               // 2 x fp32 scores [128][64]; the weights, fp16, over the first half
+constexpr uint32_t TM_O = 256;               // 2 x fp32 accumulators [128][128]
+constexpr uint32_t TMEM_COLS = 512;
+constexpr long long WAIT_LIMIT = 2000000000ll;  // clock cycles (~1 s)
+constexpr float LAZY = 8.0f;    // log2 headroom before the reference moves
+// weights are 2^(s - reference + WSHIFT) <= 2^14: normal fp16 numbers down to 2^-20 of the reference
+constexpr float WSHIFT = 6.0f;
+
+__host__ __device__ constexpr int row_bytes(int bits) { return bits == 8 ? D : D * bits / 8; }
+// Shared memory (offsets from a 1024-byte aligned base).
+__host__ __device__ constexpr uint32_t lut_bytes(int bits) { return bits == 8 ? 0u : 32u * 4u * (1u << (2 * bits)); }
+// 4-bit key pairs: 256-byte rows, so that a lookup address is one byte
+// permute of the code word (the code byte in bits 8-15, the lane's offset
+// below) and the load's immediate offset holds the table's shared-window
+// address (dynamic shared memory begins at window address SMEM_WINDOW, which
+// the host checks).
+constexpr uint32_t SMEM_WINDOW = 1024;
+__host__ __device__ constexpr bool wide(int kb) { return kb == 4; }
+__host__ __device__ constexpr uint32_t klut_bytes(int kb) { return wide(kb) ? 65536u : lut_bytes(kb); }
+constexpr int SCHED_MAX = 4096;                             // most units the shared schedule holds
+constexpr uint32_t SM_K = 0;                                // 2 x fp16 K~ [64][128]
+constexpr uint32_t SM_V = SM_K + 2 * BK * D * 2;            // 2 x fp16 V~ [64][128]
+constexpr uint32_t SM_KNR = SM_V + 2 * BK * D * 2;          // fp32 key norms of the last four tiles
+constexpr uint32_t SM_AMAX = SM_KNR + 4 * BK * 4;           // float [2][128]: largest |q~| of each half row
+constexpr uint32_t SM_ML = SM_AMAX + 2 * BM * 4;            // float [2][2][128]: a stream's references and sums
+constexpr uint32_t SM_CENT = SM_ML + 4 * BM * 4;            // fp16 centroids, keys then values
+constexpr uint32_t SM_BAR = SM_CENT + 64;
+constexpr int B_FULL = 0, B_EMPTY = NS, B_KFULL = 2 * NS, B_KEMPTY = B_KFULL + 2, B_VFULL = B_KEMPTY + 2,
+              B_PV = B_VFULL + 2, B_SFULL = B_PV + 2, B_PFULL = B_SFULL + 2, B_QREADY = B_PFULL + 2,
+              B_FINAL = B_QREADY + 1, NBARS = B_FINAL + 1;
+constexpr uint32_t SM_TMEM = SM_BAR + NBARS * 8;
+constexpr uint32_t SM_FLAG = SM_TMEM + 4;
+constexpr uint32_t SM_SEG = (SM_FLAG + 4 + 15) & ~15u;      // uint32 [5]: g0, g1, the end for empty units, C, first unit
+constexpr uint32_t SM_SCAN = SM_SEG + 32;
+constexpr uint32_t SM_SCHED = SM_SCAN + NTHREADS * 4;       // uint32 [units + 1]: tiles before each unit
+constexpr uint32_t SM_KLUT = (SM_SCHED + (SCHED_MAX + 1) * 4 + 127) & ~127u;
+__host__ __device__ constexpr uint32_t sm_vlut(int kb) { return SM_KLUT + klut_bytes(kb); }
+__host__ __device__ constexpr uint32_t sm_stage(int kb, int vb) { return sm_vlut(kb) + lut_bytes(vb); }
+__host__ __device__ constexpr uint32_t stage_bytes(int kb, int vb) {
+    return BK * (row_bytes(kb) + row_bytes(vb) + 4);  // K codes, V codes, K norms, V norms
+}
+__host__ __device__ constexpr uint32_t sm_alloc(int kb, int vb) {
+    return sm_stage(kb, vb) + NS * stage_bytes(kb, vb) + 1024;
+}
+static_assert(sm_alloc(4, 4) <= 227u * 1024u && sm_alloc(4, 8) <= 227u * 1024u && sm_alloc(8, 8) <= 227u * 1024u,
+              "the largest layouts fit a block's shared memory");
+
+__device__ __forceinline__ uint32_t pack2(uint16_t lo, uint16_t hi) { return lo | (static_cast<uint32_t>(hi) << 16); }
+
+// ------------------------------------------------------------ the schedule
+struct Segment {
+    int u, j0, j1;
+};
+
+// The block's share of the tile sequence as segments (unit, tiles [j0, j1)):
+// P[u] tiles come before unit u, block c of C takes [c total / C,
+// (c + 1) total / C); a unit without tiles belongs to the block whose range
+// holds its start.  Without a schedule block c is unit c, whole.
+__device__ __forceinline__ bool next_segment(const Args& a, const uint8_t* smem, int& it, Segment& s) {
+    const volatile uint32_t* seg = reinterpret_cast<const volatile uint32_t*>(smem + SM_SEG);
+    if (it < 0) it = static_cast<int>(seg[4]);
+    if (it >= a.units) return false;
+    s.u = it;
+    if (!a.spread) {
+        if (it != static_cast<int>(blockIdx.x)) return false;
+        s.j0 = 0;
+        s.j1 = unit_of<BK>(a, it).ntiles;
+    } else {
+        const volatile uint32_t* P = reinterpret_cast<const volatile uint32_t*>(smem + SM_SCHED);
+        const uint32_t pu = P[it], pn = P[it + 1], g0 = seg[0], g1 = seg[1];
+        if (pu >= seg[2]) return false;
+        s.j0 = static_cast<int>((pu > g0 ? pu : g0) - pu);
+        s.j1 = static_cast<int>((pn < g1 ? pn : g1) - pu);
+    }
+    ++it;
+    return true;
+}
+
+// The block whose range holds global tile g (g < total).
+__device__ __forceinline__ int block_of(uint32_t g, uint32_t total, uint32_t nblocks) {
+    return static_cast<int>(((static_cast<uint64_t>(g) + 1) * nblocks - 1) / total);
+}
+// A block holds at most two pieces of cut units: the head of the unit its
+// range starts (slot 2c + 1) and a piece of a unit begun earlier (slot 2c).
+// A slot is [BM][D] fp32 rows, then m and l.
+constexpr size_t PART_FLOATS = static_cast<size_t>(BM) * (D + 2);
+__device__ __forceinline__ int part_slot(int block, int first_block) { return 2 * block + (block == first_block); }
+
+// --------------------------------------------------------------- dequantise
+template <int BITS, int ROW = 32>
+__device__ void build_lut(uint32_t* lut, const uint16_t* cent, int t, int nthreads) {
+    constexpr int n = 32 << (2 * BITS), m = (1 << BITS) - 1;
+    for (int i = t; i < n; i += nthreads) {
+        const int e = i >> 5;
+        lut[e * ROW + (i & 31)] = pack2(cent[e & m], cent[e >> BITS]);
+    }
+}
+
+// Four int8 bytes as two fp16 pairs: the byte with its top bit flipped is the
+// mantissa of 1024, 1152 + b; subtracting 1152 is exact.
+__device__ __forceinline__ uint2 int8_to_half(uint32_t b) {
+    const uint32_t x = b ^ 0x80808080u, k = 0x64646464u;
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t lo = __byte_perm(x, k, 0x4140), hi = __byte_perm(x, k, 0x4342);
+    const __half2 p = __hsub2(*reinterpret_cast<__half2*>(&lo), off), q = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+}
+
+// One operand tile [64 slots][128 channels] from a stage's rows: this thread
+// takes channel group dt % 16 (8 channels) of slots dt / 16 + 16 i.  SCALE:
+// times the slot's fp16 norm.  Slots at or past nk are zeros.
+template <int BITS, bool SCALE, bool WIDE>
+__device__ __forceinline__ void dequant_tile(uint32_t tile, uint32_t codes, uint32_t lut, uint32_t snorms,
+                                             const uint16_t* gnorms, bool staged, int dt, int nk) {
+    constexpr int RB = row_bytes(BITS), W = 2 * BITS, IT = BK * (D / 8) / (DEQ_WARPS * 32);
+    constexpr uint32_t M = (1u << W) - 1;
+    const int cg = dt & 15, k0 = dt >> 4;
+    uint4 v[IT];
+    if constexpr (BITS == 8) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const uint32_t at = codes + (k0 + 16 * i) * RB + 8 * cg;
+            const uint2 p = int8_to_half(ptx::lds32(at)), q = int8_to_half(ptx::lds32(at + 4));
+            v[i] = make_uint4(p.x, p.y, q.x, q.y);
+        }
+    } else {
+        uint32_t c8[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const uint32_t row = codes + (k0 + 16 * i) * RB;
+            if constexpr (BITS == 4) {
+                c8[i] = ptx::lds32(row + 4 * cg);
+            } else if constexpr (BITS == 2) {
+                c8[i] = ptx::lds16(row + 2 * cg);
+            } else {  // 24 bits from bit 24 cg: may straddle two words
+                const int bit = 24 * cg, w = bit >> 5, sh = bit & 31;
+                const uint32_t lo = ptx::lds32(row + 4 * w), hi = ptx::lds32(row + 4 * min(w + 1, RB / 4 - 1));
+                c8[i] = __funnelshift_r(lo, hi, sh);
+            }
+        }
+        if constexpr (WIDE) {
+            const uint32_t l4 = 4u * static_cast<uint32_t>(dt & 31);
+            constexpr uint32_t T = SMEM_WINDOW + SM_KLUT;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                v[i].x = ptx::lds32_imm<T>(__byte_perm(c8[i], l4, 0x7604));
+                v[i].y = ptx::lds32_imm<T>(__byte_perm(c8[i], l4, 0x7614));
+                v[i].z = ptx::lds32_imm<T>(__byte_perm(c8[i], l4, 0x7624));
+                v[i].w = ptx::lds32_imm<T>(__byte_perm(c8[i], l4, 0x7634));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                v[i].x = ptx::lds32(lut + 128u * (c8[i] & M));
+                v[i].y = ptx::lds32(lut + 128u * ((c8[i] >> W) & M));
+                v[i].z = ptx::lds32(lut + 128u * ((c8[i] >> (2 * W)) & M));
+                v[i].w = ptx::lds32(lut + 128u * ((c8[i] >> (3 * W)) & M));
+            }
+        }
+    }
+    if constexpr (SCALE) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int key = k0 + 16 * i;
+            uint32_t nb = staged ? ptx::lds16(snorms + 2 * key) : (key < nk ? gnorms[key] : uint16_t(0));
+            // (a norm that is not finite: the row is zeros, its key's score NaN)
+            if ((nb & 0x7C00u) == 0x7C00u) nb = 0u;
+            const uint32_t n2 = nb | (nb << 16);
+            const __half2 f = *reinterpret_cast<const __half2*>(&n2);
+            __half2* h = reinterpret_cast<__half2*>(&v[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
+        }
+    }
+    if (nk < BK) {  // the last, partial tile only
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+            if (k0 + 16 * i >= nk) v[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) ptx::sts128(tile + tc::sw128_offset(k0 + 16 * i, 8 * cg, BK), v[i]);
+}
+
+// Walsh-Hadamard butterflies over 64 values.
+__device__ __forceinline__ void fwht64(float (&x)[64]) { fwht_registers(x); }
+
+// This half's 64 values of a query row after the first butterfly stage
+// (x[i] +- x[i + 64], signs applied), or (int8 keys) the half itself.
+__device__ __forceinline__ void load_half(const Args& a, size_t off, int half, bool rotate, float (&x)[64]) {
+    if (!rotate) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+            float v[4];
+            load4(a.q, off + 64 * half + c, a.q_dtype, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[c + e] = v[e];
+            if (c % 16 == 12) asm volatile("" ::: "memory");
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 64; c += 4) {
+        float lo[4], hi[4];
+        load4(a.q, off + c, a.q_dtype, lo);
+        load4(a.q, off + 64 + c, a.q_dtype, hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float p = flip_sign(lo[e], (a.signs[(c + e) >> 5] >> ((c + e) & 31)) & 1u);
+            const float q = flip_sign(hi[e], (a.signs[2 + ((c + e) >> 5)] >> ((c + e) & 31)) & 1u);
+            x[c + e] = half ? p - q : p + q;
+        }
+        // (a few loads in flight at a time: all of them together would not fit the registers)
+        if (c % 16 == 12) asm volatile("" ::: "memory");
+    }
+}
+
+// 8 consecutive fp32 columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void ld_8cols(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int KB, int VB>
+__global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_constant__ Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = ptx::smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t bars = sbase + SM_BAR;
+    auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM_FLAG);
+    auto fail = [&]() {
+        if (!*abort_flag && a.err) atomicOr(a.err, TQ_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+    };
+    auto wait = [&](int i, uint32_t parity) -> bool {
+        if (*abort_flag) return false;
+        if (!ptx::mbar_wait_bounded_lean(bar(i), parity, WAIT_LIMIT)) {
+            fail();
+            return false;
+        }
+        return true;
+    };
+    const int G = a.group;
+    // softmax warps of a stream that own query rows
+    const int aw = (min(BM, min(a.tok_per_tile, a.n_draft) * G) + 31) / 32;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            ptx::mbar_init(bar(B_FULL + i), 1);
+            ptx::mbar_init(bar(B_EMPTY + i), DEQ_WARPS);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(B_KFULL + i), DEQ_WARPS);
+            ptx::mbar_init(bar(B_KEMPTY + i), 1);
+            ptx::mbar_init(bar(B_VFULL + i), DEQ_WARPS);
+            ptx::mbar_init(bar(B_PV + i), 1);
+            ptx::mbar_init(bar(B_SFULL + i), 1);
+            ptx::mbar_init(bar(B_PFULL + i), aw);
+        }
+        ptx::mbar_init(bar(B_QREADY), 2 * aw);
+        ptx::mbar_init(bar(B_FINAL), 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (tid < 32) reinterpret_cast<uint16_t*>(smem + SM_CENT)[tid] = tid < 16 ? a.kcent[tid] : a.vcent[tid - 16];
+    if (warp == MMA_WARP) {
+        tc::tmem_alloc(sbase + SM_TMEM, TMEM_COLS);
+        tc::tmem_relinquish();
+    }
+    __syncthreads();
+    if (warp >= DEQ0 / 32 && warp < LIGHT0 / 32) {
+        const uint16_t* kcent = reinterpret_cast<const uint16_t*>(smem + SM_CENT);
+        if constexpr (KB < 8)
+            build_lut<KB, wide(KB) ? 64 : 32>(reinterpret_cast<uint32_t*>(smem + SM_KLUT), kcent, tid - DEQ0, DEQ_WARPS * 32);
+        if constexpr (VB < 8)
+            build_lut<VB>(reinterpret_cast<uint32_t*>(smem + sm_vlut(KB)), kcent + 16, tid - DEQ0, DEQ_WARPS * 32);
+    }
+    // everything above overlaps the end of the kernel before; nothing of the
+    // caller's memory has been read or written yet
+    ptx::wait_prerequisites();
+    ptx::launch_dependents();
+
+    // ---- the schedule: P[u] = tiles of the units before u
+    uint32_t* P = reinterpret_cast<uint32_t*>(smem + SM_SCHED);
+    uint32_t* scan = reinterpret_cast<uint32_t*>(smem + SM_SCAN);
+    const int U = a.units;
+    if (a.spread) {
+        const int per = (U + NTHREADS - 1) / NTHREADS, u0 = min(U, tid * per), u1 = min(U, u0 + per);
+        uint32_t sum = 0;
+        for (int u = u0; u < u1; ++u) sum += static_cast<uint32_t>(unit_of<BK>(a, u).ntiles);
+        scan[tid] = sum;
+        __syncthreads();
+        if (warp == 0) {
+            constexpr int PER_LANE = NTHREADS / 32;
+            uint32_t t = 0;
+            for (int i = 0; i < PER_LANE; ++i) t += scan[lane * PER_LANE + i];
+            uint32_t incl = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(kFullMask, incl, o);
+                if (lane >= o) incl += y;
+            }
+            uint32_t run = incl - t;
+            for (int i = 0; i < PER_LANE; ++i) {
+                const uint32_t v = scan[lane * PER_LANE + i];
+                scan[lane * PER_LANE + i] = run;
+                run += v;
+            }
+            if (lane == 31) P[U] = run;
+        }
+        __syncthreads();
+        uint32_t run = scan[tid];
+        for (int u = u0; u < u1; ++u) {
+            P[u] = run;
+            run += static_cast<uint32_t>(unit_of<BK>(a, u).ntiles);
+        }
+        __syncthreads();
+        if (blockIdx.x == 0)  // (for the merge kernel)
+            for (int u = tid; u <= U; u += NTHREADS) a.sched[u] = P[u];
+    }
+    if (tid == 0) {
+        uint32_t* seg = reinterpret_cast<uint32_t*>(smem + SM_SEG);
+        const uint32_t c = blockIdx.x;
+        if (a.spread) {
+            const uint32_t total = P[U];
+            // no more sharing blocks than tiles, so that each one's range holds at least one
+            const uint32_t C = gridDim.x > total ? (total > 0 ? total : 1u) : gridDim.x;
+            const uint32_t g0 = static_cast<uint32_t>(static_cast<uint64_t>(c) * total / C);
+            const uint32_t g1 = static_cast<uint32_t>(static_cast<uint64_t>(c + 1) * total / C);
+            int lo = 0, hi = U;
+            if (c >= C) {
+                lo = U;
+            } else {  // first u with P[u + 1] > g0 or P[u] >= g0
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (P[mid + 1] > g0 || P[mid] >= g0) hi = mid;
+                    else lo = mid + 1;
+                }
+            }
+            seg[0] = g0;
+            seg[1] = g1;
+            seg[2] = c == C - 1 ? total + 1 : g1;
+            seg[3] = C;
+            seg[4] = static_cast<uint32_t>(lo);
+        } else {
+            seg[4] = c;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + SM_TMEM);
+    constexpr int kbytes = row_bytes(KB), vbytes = row_bytes(VB);
+    constexpr uint32_t STAGE = sm_stage(KB, VB), STAGE_BYTES = stage_bytes(KB, VB);
+    constexpr uint32_t ST_VC = BK * kbytes, ST_KN = ST_VC + BK * vbytes, ST_VN = ST_KN + BK * 2;
+
+    // Every role walks the same segments; tile gi (counted over the block's
+    // run) is in ring stage gi % NS and belongs to stream gi % 2.
+    if (warp >= LIGHT0 / 32) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LIGHT));
+        if (warp == PRODUCER_WARP) {
+            // -------------------------------------------------------- producer
+            const bool leader = tc::elect_one();
+            int gi = 0, it = -1;
+            Segment s;
+            while (next_segment(a, smem, it, s)) {
+                const Unit x = unit_of<BK>(a, s.u);
+                for (int j = s.j0; j < s.j1; ++j, ++gi) {
+                    const int st = gi % NS;
+                    if (gi >= NS) {
+                        if (*abort_flag) goto produced;
+                        if (!ptx::mbar_wait_bounded_sleep(bar(B_EMPTY + st), ((gi - NS) / NS) & 1, WAIT_LIMIT, 64)) {
+                            fail();
+                            goto produced;
+                        }
+                    }
+                    if (leader) {
+                        const int key0 = j * BK, nk = min(BK, x.kend - key0), n8 = (nk + 7) & ~7;
+                        const uint32_t dst = sbase + STAGE + st * STAGE_BYTES, full = bar(B_FULL + st);
+                        ptx::mbar_arrive_expect_tx(full, nk * (kbytes + vbytes) + (a.staged_norms ? n8 * 4 : 0));
+                        // one run of slots, or one per block of the pool
+                        for (int k = 0; k < nk;) {
+                            const int n = a.table ? min(nk - k, a.block_size - (key0 + k) % a.block_size) : nk;
+                            const size_t row = cache_row(a, x.b, x.kv, key0 + k);
+                            ptx::bulk_copy_g2s(dst + k * kbytes, a.k_codes + row * kbytes, n * kbytes, full);
+                            ptx::bulk_copy_g2s(dst + ST_VC + k * vbytes, a.v_codes + row * vbytes, n * vbytes, full);
+                            if (a.staged_norms) {  // (runs of norms move in 16-byte pieces)
+                                const int m8 = (n + 7) & ~7;
+                                ptx::bulk_copy_g2s(dst + ST_KN + 2 * k, a.k_norms + row, m8 * 2, full);
+                                ptx::bulk_copy_g2s(dst + ST_VN + 2 * k, a.v_norms + row, m8 * 2, full);
+                            }
+                            k += n;
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        produced:
+            // every copy issued must land before the block may exit
+            for (int k = max(0, gi - NS); k < gi; ++k)
+                ptx::mbar_wait_bounded(bar(B_FULL + k % NS), (k / NS) & 1, WAIT_LIMIT);
+        } else if (warp == MMA_WARP) {
+            // ----------------------------------------------------- MMA issuer
+            const bool leader = tc::elect_one();
+            const uint32_t idesc_s = tc::idesc_f16(BM, BK), idesc_o = tc::idesc_f16_bmn(BM, D);
+            const uint64_t kdesc0 = tc::sw128_desc(sbase + SM_K);
+            const uint64_t vdesc0 = tc::sw128_mn_desc(sbase + SM_V, BK * 128, 1024);
+            auto issue_s = [&](int gi) -> bool {
+                const int bf = gi & 1;
+                if (!wait(B_KFULL + bf, (gi >> 1) & 1)) return false;
+                tc::fence_after_sync();
+                if (leader) {
+                    const uint64_t kd = kdesc0 + static_cast<uint64_t>(bf * (BK * D * 2) >> 4);
+                    const uint32_t sd = tmem + TM_S + BK * bf;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint64_t bd = kd + static_cast<uint64_t>(((ks >> 2) * (BK * 128) + (ks & 3) * 32) >> 4);
+                        tc::mma_f16_ts(sd, tmem + TM_QHI + 8 * ks, bd, idesc_s, ks > 0);
+                        tc::mma_f16_ts(sd, tmem + TM_QLO + 8 * ks, bd, idesc_s, true);
+                    }
+                    tc::commit(bar(B_SFULL + bf));
+                    tc::commit(bar(B_KEMPTY + bf));
+                }
+                __syncwarp();
+                return true;
+            };
+            int gi = 0, qs = 0, it = -1;
+            Segment s;
+            while (next_segment(a, smem, it, s)) {
+                if (s.j1 <= s.j0) continue;
+                // the queries are in tensor memory, and the segment before has left it
+                if (!wait(B_QREADY, qs & 1)) break;
+                ++qs;
+                const int gfirst = gi, gend = gi + (s.j1 - s.j0);
+                if (!issue_s(gi)) break;
+                if (gi + 1 < gend && !issue_s(gi + 1)) break;
+                for (; gi < gend; ++gi) {
+                    const int bf = gi & 1;
+                    if (!wait(B_PFULL + bf, (gi >> 1) & 1)) goto issued;
+                    if (!wait(B_VFULL + bf, (gi >> 1) & 1)) goto issued;
+                    tc::fence_after_sync();
+                    if (leader) {
+                        const uint64_t vd = vdesc0 + static_cast<uint64_t>(bf * (BK * D * 2) >> 4);
+                        const uint32_t pa = tmem + TM_S + BK * bf;
+#pragma unroll
+                        for (int ks = 0; ks < BK / 16; ++ks)
+                            tc::mma_f16_ts(tmem + TM_O + D * bf, pa + 8 * ks, vd + static_cast<uint64_t>(ks * 2048 >> 4),
+                                           idesc_o, gi >= gfirst + 2 || ks > 0);
+                        tc::commit(bar(B_PV + bf));
+                    }
+                    __syncwarp();
+                    if (gi + 2 < gend) {
+                        // the stream's weights lie in its score buffer: they are used before it is written again
+                        if (!wait(B_PV + bf, (gi >> 1) & 1)) goto issued;
+                        if (!issue_s(gi + 2)) goto issued;
+                    }
+                }
+            }
+        issued:
+            if (leader) {
+                tc::commit(bar(B_FINAL));
+                ptx::mbar_wait_bounded(bar(B_FINAL), 0, WAIT_LIMIT);
+            }
+            __syncwarp();
+        }
+    } else if (warp >= DEQ0 / 32) {
+        // ------------------------------------------------------ dequantisers
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DEQ));
+        const int dt = tid - DEQ0;
+        const uint32_t klane = sbase + SM_KLUT + 4 * lane, vlane = sbase + sm_vlut(KB) + 4 * lane;
+        int gi = 0, it = -1;
+        Segment s;
+        while (next_segment(a, smem, it, s)) {
+            const Unit x = unit_of<BK>(a, s.u);
+            const size_t row0 = (static_cast<size_t>(x.b) * a.hkv + x.kv) * a.capacity;  // (norms that are not staged)
+            for (int j = s.j0; j < s.j1; ++j, ++gi) {
+                const int st = gi % NS, bf = gi & 1, nk = min(BK, x.kend - j * BK);
+                if (!wait(B_FULL + st, (gi / NS) & 1)) goto dequantised;
+                const uint32_t sst = sbase + STAGE + st * STAGE_BYTES;
+                const size_t row = row0 + static_cast<size_t>(j) * BK;
+                if (gi >= 2 && !wait(B_KEMPTY + bf, ((gi - 2) >> 1) & 1)) goto dequantised;
+                // the tile's key norms, for the softmax (the softmax of tile gi - 4 is done: S(gi - 2) followed it)
+                if (dt < BK) {
+                    uint16_t kn = 0, vn = 0;
+                    if (dt < nk) {
+                        kn = a.staged_norms ? ptx::lds16(sst + ST_KN + 2 * dt) : a.k_norms[row + dt];
+                        vn = a.staged_norms ? ptx::lds16(sst + ST_VN + 2 * dt) : a.v_norms[row + dt];
+                    }
+                    reinterpret_cast<float*>(smem + SM_KNR)[(gi & 3) * BK + dt] =
+                        (vn & 0x7C00u) == 0x7C00u ? NAN : half_bits_to_float(kn);
+                }
+                dequant_tile<KB, false, wide(KB)>(sbase + SM_K + bf * (BK * D * 2), sst, klane, 0u, nullptr, true, dt, nk);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_KFULL + bf));
+                if (gi >= 2 && !wait(B_PV + bf, ((gi - 2) >> 1) & 1)) goto dequantised;
+                dequant_tile<VB, true, false>(sbase + SM_V + bf * (BK * D * 2), sst + ST_VC, vlane, sst + ST_VN,
+                                              a.v_norms + row, a.staged_norms != 0, dt, nk);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(bar(B_VFULL + bf));
+                    ptx::mbar_arrive(bar(B_EMPTY + st));
+                }
+            }
+        }
+    dequantised:;
+    } else {
+        // ---------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+        const int g = warp >> 2, r = tid & 127;  // stream, query row
+        const int rt = r / G, rh = r % G;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        constexpr float rsqrt_d = 0.08838834764831845f;
+        float* amax = reinterpret_cast<float*>(smem + SM_AMAX);
+        float* ml = reinterpret_cast<float*>(smem + SM_ML);
+        int gi = 0, it = -1;
+        Segment s;
+        if ((warp & 3) >= aw) it = U;  // no rows: the warp takes no part
+        while (next_segment(a, smem, it, s)) {
+            const Unit x = unit_of<BK>(a, s.u);
+            const bool row_ok = rt < x.ntok && rt * G + rh < BM;
+            const size_t qoff = ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + rt) * a.hq + x.kv * G + rh) * D;
+            if (s.j1 <= s.j0) {
+                // no tiles: a refused sequence, or one without drafts in this unit
+                if (x.bad) {
+                    if (x.qt == 0 && x.kv == 0 && tid == 0 && a.err) atomicOr(a.err, TQ_DEVERR_SEQLEN);
+                    if (rt < min(a.tok_per_tile, a.n_draft - x.tok0) && rt * G + rh < BM) {
+                        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 8) store_row<8>(a.out, qoff + 64 * g + c, z, a.out_dtype);
+                    }
+                }
+                continue;
+            }
+            float qscale;
+            {
+                // ---- this stream's half of the row's queries
+                float q[64];
+                if (row_ok) {
+                    load_half(a, qoff, g, KB < 8, q);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) q[i] = 0.f;
+                }
+                __syncwarp();
+                if constexpr (KB < 8) fwht64(q);
+                float m = 0.f;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(q[i]));
+                amax[g * BM + r] = m;
+                // (after a wait that ran out every softmax warp leaves at the
+                // same barrier)
+                if (ptx::named_barrier_or(2, 2 * aw * 32, *abort_flag != 0)) goto softmax_done;
+                m = fmaxf(m, amax[(1 - g) * BM + r]);
+                qscale = KB < 8 ? m * rsqrt_d : m;
+                const float inv = m > 0.f ? 1.f / m : 0.f;
+#pragma unroll
+                for (int c = 0; c < 64; c += 16) {
+                    uint32_t hw[8], lw[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v0 = q[c + 2 * e] * inv, v1 = q[c + 2 * e + 1] * inv;
+                        const __half h0 = __float2half_rn(v0), h1 = __float2half_rn(v1);
+                        hw[e] = pack2(__half_as_ushort(h0), __half_as_ushort(h1));
+                        lw[e] = ptx::pack_half2(v0 - __half2float(h0), v1 - __half2float(h1));
+                    }
+                    tc::st_8cols(tmem + lanes + TM_QHI + 32 * g + c / 2, hw);
+                    tc::st_8cols(tmem + lanes + TM_QLO + 32 * g + c / 2, lw);
+                }
+            }
+            tc::st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(B_QREADY));
+            const float rs = fmaxf(qscale * a.score_scale, 1e-30f);  // (keeps a masked -inf score -inf)
+            const uint64_t mask = row_ok ? row_mask(a, x, x.tok0 + rt) : 0ull;
+            float mref = NOTHING, l = 0.f;
+            bool dead = false;
+            const int gfirst = gi, gend = gi + (s.j1 - s.j0);
+            gi += (gi & 1) != g;  // the stream's first tile of the segment
+            for (; gi < gend; gi += 2) {
+                dead = !wait(B_SFULL + g, (gi >> 1) & 1);
+                if (dead) break;
+                tc::fence_after_sync();
+                float sc[BK];
+                {
+                    float (&sc0)[32] = *reinterpret_cast<float (*)[32]>(&sc[0]);
+                    float (&sc1)[32] = *reinterpret_cast<float (*)[32]>(&sc[32]);
+                    tc::ld_32cols(tmem + lanes + TM_S + BK * g, sc0);
+                    tc::ld_32cols(tmem + lanes + TM_S + BK * g + 32, sc1);
+                }
+                tc::ld_wait();
+                const float4* kn4 = reinterpret_cast<const float4*>(smem + SM_KNR + (gi & 3) * BK * 4);
+#pragma unroll
+                for (int i = 0; i < BK; i += 4) {
+                    const float4 k4 = kn4[i / 4];
+                    const float2 a01 = ptx::fmul2(make_float2(sc[i], sc[i + 1]), make_float2(k4.x, k4.y));
+                    const float2 a23 = ptx::fmul2(make_float2(sc[i + 2], sc[i + 3]), make_float2(k4.z, k4.w));
+                    sc[i] = a01.x;
+                    sc[i + 1] = a01.y;
+                    sc[i + 2] = a23.x;
+                    sc[i + 3] = a23.y;
+                }
+                const int key0 = (s.j0 + gi - gfirst) * BK;
+                if (key0 + BK > x.base) {  // a tile with drafts: the tree's mask
+                    const uint64_t v = visible(mask, key0, x.base);
+                    const uint32_t v0 = static_cast<uint32_t>(v), v1 = static_cast<uint32_t>(v >> 32);
+#pragma unroll
+                    for (int i = 0; i < BK; ++i)
+                        if (!(((i < 32 ? v0 : v1) >> (i & 31)) & 1u)) sc[i] = -INFINITY;
+                }
+                float m4[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float m = sc[16 * q];
+#pragma unroll
+                    for (int i = 1; i < 15; i += 2) m = ptx::fmax3(m, sc[16 * q + i], sc[16 * q + i + 1]);
+                    m4[q] = fmaxf(m, sc[16 * q + 15]);
+                }
+                const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rs;
+                const bool need = mt > mref + LAZY;
+                if (__any_sync(kFullMask, need)) {
+                    const float mnew = need ? mt : mref;
+                    const float c = ptx::ex2(mref - mnew);
+                    if (gi >= gfirst + 2) {
+                        // (scores of this tile came after the stream's last P V: its accumulator is complete)
+#pragma unroll 1
+                        for (int q8 = 0; q8 < 8; ++q8) {
+                            float ov[16];
+                            tc::ld_16cols(tmem + lanes + TM_O + D * g + 16 * q8, ov);
+                            tc::ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) ov[i] *= c;
+                            tc::st_16cols(tmem + lanes + TM_O + D * g + 16 * q8, ov);
+                        }
+                    }
+                    l *= c;
+                    mref = mnew;
+                }
+                const float2 rs2 = make_float2(rs, rs), nm2 = make_float2(WSHIFT - mref, WSHIFT - mref);
+                float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float2 t0 = ptx::ffma2(make_float2(sc[32 * h + i], sc[32 * h + i + 1]), rs2, nm2);
+                        const float2 t1 = ptx::ffma2(make_float2(sc[32 * h + i + 2], sc[32 * h + i + 3]), rs2, nm2);
+                        const float2 p0 = make_float2(ptx::ex2(t0.x), ptx::ex2(t0.y));
+                        const float2 p1 = make_float2(ptx::ex2(t1.x), ptx::ex2(t1.y));
+                        acc0 = ptx::fadd2(acc0, p0);
+                        acc1 = ptx::fadd2(acc1, p1);
+                        pw[i / 2] = ptx::pack_half2(p0.x, p0.y);
+                        pw[i / 2 + 1] = ptx::pack_half2(p1.x, p1.y);
+                    }
+                    tc::st_16cols_u(tmem + lanes + TM_S + BK * g + 16 * h, pw);
+                }
+                l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                tc::st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_PFULL + g));
+            }
+            // ---- the segment's end: the stream's last P V, then both streams
+            // are joined (each warp takes half of the channels)
+            {
+                const int last = gend - 1 - ((gend - 1 - g) & 1);  // the stream's last tile, if it had one
+                if (!dead && last >= gfirst) dead = !wait(B_PV + g, (last >> 1) & 1);
+                gi = gend;
+                ml[g * BM + r] = mref;
+                ml[(2 + g) * BM + r] = l;
+            }
+            if (ptx::named_barrier_or(2, 2 * aw * 32, dead)) goto softmax_done;
+            tc::fence_after_sync();
+            {
+                const float mo = ml[(1 - g) * BM + r], lo = ml[(3 - g) * BM + r];
+                const float M = fmaxf(mref, mo);
+                const float wm = ptx::ex2(mref - M), wo = ptx::ex2(mo - M);
+                const float L = l * wm + lo * wo;
+                const float w0 = g ? wo : wm, w1 = g ? wm : wo;  // weights of streams 0 and 1
+                const bool two = s.j1 - s.j0 > 1;                // (with one tile the other accumulator holds nothing)
+                const int only = gfirst & 1;                     // the stream of the first tile
+                // 8 joined channels from column c
+                auto joined = [&](int c, float (&v)[8]) {
+                    float u[8];
+                    ld_8cols(tmem + lanes + TM_O + D * only + c, v);
+                    if (two) ld_8cols(tmem + lanes + TM_O + D * (1 - only) + c, u);
+                    tc::ld_wait();
+                    const float wv = only ? w1 : w0, wu = only ? w0 : w1;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = two ? v[i] * wv + u[i] * wu : v[i] * wv;
+                };
+                const volatile uint32_t* seg = reinterpret_cast<const volatile uint32_t*>(smem + SM_SEG);
+                const bool cut = a.spread && (P[s.u] < seg[0] || P[s.u + 1] > seg[1]);
+                if (cut) {
+                    const int cb = static_cast<int>(blockIdx.x), ca = block_of(P[s.u], P[U], seg[3]);
+                    float* mine = a.parts + static_cast<size_t>(part_slot(cb, ca)) * PART_FLOATS;
+#pragma unroll 1
+                    for (int c = 64 * g; c < 64 * g + 64; c += 8) {
+                        float v[8];
+                        joined(c, v);
+                        if (row_ok) {
+#pragma unroll
+                            for (int i = 0; i < 8; i += 4)
+                                *reinterpret_cast<float4*>(mine + r * D + c + i) =
+                                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        }
+                        __syncwarp();
+                    }
+                    if (g == 0 && row_ok) {
+                        mine[BM * D + r] = piece_reference(M, L);
+                        mine[BM * D + BM + r] = L;
+                    }
+                } else {
+                    float o[64];
+                    const float inv = (L == 0.f ? 0.f : a.out_scale / L) * (VB < 8 ? rsqrt_d : 1.f);
+                    if constexpr (VB < 8) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 8) {
+                            float v[8], u[8];
+                            joined(c, v);
+                            joined(64 + c, u);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[c + i] = g ? v[i] - u[i] : v[i] + u[i];
+                        }
+                        fwht64(o);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 8) {
+                            float v[8];
+                            joined(64 * g + c, v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[c + i] = v[i];
+                        }
+                    }
+                    if (row_ok) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 8) {
+                            float y[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int i = c + e;
+                                y[e] = o[i] * inv;
+                                if constexpr (VB < 8) y[e] = flip_sign(y[e], (a.signs[2 * g + (i >> 5)] >> (i & 31)) & 1u);
+                            }
+                            store_row<8>(a.out, qoff + 64 * g + c, y, a.out_dtype);
+                        }
+                    }
+                }
+            }
+            tc::fence_before_sync();
+        }
+    softmax_done:;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+template <typename... PP, typename... T>
+static cudaError_t launch_dependent(void (*kernel)(PP...), dim3 grid, dim3 block, uint32_t smem_bytes, cudaStream_t s,
+                                    T&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem_bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<T&&>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int KB, int VB>
+cudaError_t launch_typed(const Args& a, int blocks, cudaStream_t s) {
+    constexpr uint32_t bytes = sm_alloc(KB, VB);
+    const cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bytes));
+    if (e != cudaSuccess) return e;
+    return launch_dependent(tree_mma_kernel<KB, VB>, dim3(static_cast<unsigned>(blocks)), dim3(NTHREADS), bytes, s, a);
+}
+
+}  // namespace mma
+
+// The tensor-memory kernel for keys of 2, 3, 4 bits or int8 (one source file each).
+cudaError_t launch_mma_k2(int vb, const Args& a, int blocks, cudaStream_t s);
+cudaError_t launch_mma_k3(int vb, const Args& a, int blocks, cudaStream_t s);
+cudaError_t launch_mma_k4(int vb, const Args& a, int blocks, cudaStream_t s);
+cudaError_t launch_mma_k8(int vb, const Args& a, int blocks, cudaStream_t s);
+
+}  // namespace tree
+}  // namespace tq
