@@ -311,9 +311,9 @@ __global__ void __launch_bounds__(MERGE_THREADS) tree_general_merge_kernel(const
     if (t >= rows) return;
     const float* first = a.parts + static_cast<size_t>(blockIdx.x) * a.n_split * (GEN_ROWS * (D + 2));
     const size_t dst = ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + t) * a.hq + x.kv * G + g) * D;
-    merge_row<D, GEN_ROWS>(
-        a, [&](int j) { return first + static_cast<size_t>(j) * (GEN_ROWS * (D + 2)); }, x.bad ? 0 : a.n_split, r, dst,
-        true);
+    merge_row<D>(
+        a, [&](int j) { return first + static_cast<size_t>(j) * (GEN_ROWS * (D + 2)); }, x.bad ? 0 : a.n_split, GEN_ROWS,
+        r, dst);
 }
 
 // The rows of the units that the tensor-memory kernel cut between blocks
@@ -332,35 +332,41 @@ __global__ void __launch_bounds__(MERGE_THREADS) tree_mma_merge_kernel(const __g
     const int G = a.group, t = r / G, g = r % G;
     if (t >= x.ntok) return;
     const size_t dst = ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + t) * a.hq + x.kv * G + g) * mma::D;
-    merge_row<mma::D, mma::BM>(
-        a, [&](int j) { return a.parts + static_cast<size_t>(mma::part_slot(ca + j, ca)) * mma::PART_FLOATS; },
-        cz - ca + 1, r, dst, true);
+    const size_t slot = mma::part_floats(a.part_rows);
+    merge_row<mma::D>(
+        a, [&](int j) { return a.parts + static_cast<size_t>(mma::part_slot(ca + j, ca)) * slot; }, cz - ca + 1,
+        a.part_rows, r, dst);
 }
 
 // Work layout of a call.  general: n_split blocks per unit of GEN_ROWS rows.
-// Tensor-memory kernel: units of up to 128 rows (a sequence's drafts spread
-// evenly over its units), the tile sequence shared by one block per SM
-// (spread) or, past SCHED_MAX units, a block per unit; workspace: the schedule,
-// then two partial outputs per block.
+// Tensor-memory kernel: units of up to 128 rows, or (pair) 256 where a kv head
+// has more than 128 (its drafts spread evenly over its units), the
+// tile sequence shared by one block per SM (spread) or, past SCHED_MAX units,
+// a block per unit; workspace: the schedule, then two partial outputs per
+// block.
 struct Plan {
     long long units;
-    int tok_per_tile, qtiles, n_split, spread, blocks;
+    int tok_per_tile, qtiles, n_split, spread, blocks, pair, part_rows;
     size_t sched_bytes, bytes;
 };
 
 static bool mma_supported(const tq_params& p) { return p.head_dim == mma::D && p.qjl_dims == 0; }
 
-static Plan mma_plan(const tq_params& p, int batch, int n_draft, int sms) {
+static Plan mma_plan(const tq_params& p, int batch, int n_draft, int sms, bool may_pair) {
     Plan pl{};
-    const int most = mma::BM / (p.num_q_heads / p.num_kv_heads);
+    const int group = p.num_q_heads / p.num_kv_heads;
+    pl.pair = may_pair && n_draft > mma::BM / group;
+    const int most = (pl.pair ? 2 * mma::BM : mma::BM) / group;
     pl.qtiles = (n_draft + most - 1) / most;
     pl.tok_per_tile = (n_draft + pl.qtiles - 1) / pl.qtiles;
+    pl.pair = pl.pair && pl.tok_per_tile * group > mma::BM;
+    pl.part_rows = (pl.tok_per_tile * group + 31) / 32 * 32;
     pl.units = static_cast<long long>(batch) * p.num_kv_heads * pl.qtiles;
     pl.spread = pl.units <= mma::SCHED_MAX;
     pl.blocks = pl.spread ? sms : static_cast<int>(pl.units);
     if (pl.spread) {
         pl.sched_bytes = (static_cast<size_t>(pl.units + 1) * 4 + 255) / 256 * 256;
-        pl.bytes = pl.sched_bytes + 2ull * pl.blocks * mma::PART_FLOATS * sizeof(float);
+        pl.bytes = pl.sched_bytes + 2ull * pl.blocks * mma::part_floats(pl.part_rows) * sizeof(float);
     }
     return pl;
 }
@@ -403,8 +409,9 @@ static cudaError_t launch_mma(const Args& a, const Plan& pl, cudaStream_t s) {
                                  dim3(MERGE_THREADS), 0u, s, a, pl.blocks);
 }
 
-static Plan plan_of(const tq_params& p, int batch, int n_draft, int sms) {
-    return mma_supported(p) ? mma_plan(p, batch, n_draft, sms) : general_plan(p, batch, n_draft, sms);
+static Plan plan_of(const tq_params& p, int batch, int n_draft, int sms, int out_dtype) {
+    return mma_supported(p) ? mma_plan(p, batch, n_draft, sms, out_dtype == TQ_BF16)
+                            : general_plan(p, batch, n_draft, sms);
 }
 
 static tq_status attend(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const void* d_q,
@@ -428,7 +435,7 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     if (sms <= 0) return TQ_ERR_CUDA;
     const int capacity = pm ? pm->max_blocks * pm->block_size : cache->capacity;
     const bool mm = mma_supported(p);
-    Plan pl = plan_of(p, batch, n_draft, sms);
+    Plan pl = plan_of(p, batch, n_draft, sms, out_dtype);
     if (pl.units > INT32_MAX) return TQ_ERR_INVALID_ARG;
     if (mm && pl.spread && pl.units * ((capacity + mma::BK - 1) / mma::BK) >= (1ll << 31)) {
         // the shared tile sequence is counted in 32 bits: a block per unit instead
@@ -441,8 +448,7 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
         if (workspace_bytes < pl.bytes) return TQ_ERR_CAPACITY;
         if (!aligned16(d_workspace)) return TQ_ERR_ALIGNMENT;
     }
-    if (mm && mma::wide(p.k_mode == TQ_MODE_INT8 ? 8 : p.k_bits)) {
-        // the 4-bit key table's lookups carry its shared-window address
+    if (mm) {  // (the code tables' lookups carry their shared-window addresses)
         int reserved = 0, dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess)
@@ -487,6 +493,8 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     a.units = static_cast<int>(pl.units);
     a.n_split = pl.n_split;
     a.spread = pl.spread;
+    a.pair = pl.pair;
+    a.part_rows = pl.part_rows;
     a.staged_norms = pm || capacity % 8 == 0;
     const double rd = std::sqrt(static_cast<double>(p.head_dim));
     const double sm = p.sm_scale > 0.0f ? static_cast<double>(p.sm_scale) : 1.0 / rd;
@@ -531,7 +539,10 @@ tq_status tq_tree_workspace_bytes(const tq_params* params, int32_t batch, int32_
     if (n_draft > tree::MAX_DRAFTS) return TQ_ERR_UNSUPPORTED;
     const int sms = num_sms_current();
     if (sms <= 0) return TQ_ERR_CUDA;
-    *bytes = tree::plan_of(*params, batch, n_draft, sms).bytes;
+    // (for every output type)
+    const size_t a = tree::plan_of(*params, batch, n_draft, sms, TQ_BF16).bytes;
+    const size_t b = tree::plan_of(*params, batch, n_draft, sms, TQ_F32).bytes;
+    *bytes = a > b ? a : b;
     return TQ_OK;
 }
 

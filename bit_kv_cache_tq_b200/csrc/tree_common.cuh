@@ -43,6 +43,7 @@ struct Args {
     int k_bits, v_bits, qjl_dims;  // 8 bits: an int8 side
     int staged_norms;              // rows of norms are 16-byte aligned every 8 slots
     int tok_per_tile, qtiles, units, n_split, spread;
+    int pair, part_rows;           // (tensor-memory kernel) two row blocks a unit; rows of a partial output's slot
     float score_scale, out_scale, key_scale;
     uint32_t signs[8];
     uint16_t kcent[16], vcent[16];  // fp16 centroids (tensor-memory kernel)
@@ -137,14 +138,14 @@ __device__ __forceinline__ void store_row(void* base, size_t off, const float (&
 // (log2 units) and the sum l_j;
 //   out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j,  M = max_j m_j,
 // then the inverse rotation (turbo values).  piece(j) gives a piece's rows
-// [ROWS][D], then [ROWS] m, then [ROWS] l.  A row that saw nothing is zero.
+// [rows][D], then [rows] m, then [rows] l.  A row that saw nothing is zero.
 constexpr int MERGE_BATCH = 16;
-template <int D, int ROWS, typename Piece>
-__device__ __forceinline__ void merge_row(const Args& a, Piece piece, int np, int r, size_t dst, bool store) {
+template <int D, typename Piece>
+__device__ __forceinline__ void merge_row(const Args& a, Piece piece, int np, int rows, int r, size_t dst) {
     constexpr int N = D / 32;
     const int lane = static_cast<int>(threadIdx.x) & 31;
     float M = -INFINITY;
-    for (int j = lane; j < np; j += 32) M = fmaxf(M, __ldcg(piece(j) + ROWS * D + r));
+    for (int j = lane; j < np; j += 32) M = fmaxf(M, __ldcg(piece(j) + rows * D + r));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
     float L = 0.f, e[N];
@@ -154,10 +155,10 @@ __device__ __forceinline__ void merge_row(const Args& a, Piece piece, int np, in
         float w = 0.f;  // the weight of piece j0 + lane
         if (j0 + lane < np) {
             const float* sp = piece(j0 + lane);
-            const float mk = __ldcg(sp + ROWS * D + r);
+            const float mk = __ldcg(sp + rows * D + r);
             if (mk > -INFINITY) {
                 w = ptx::ex2(mk - M);
-                L = fmaf(__ldcg(sp + ROWS * D + ROWS + r), w, L);
+                L = fmaf(__ldcg(sp + rows * D + rows + r), w, L);
             }
         }
         const int nj = min(32, np - j0);
@@ -194,7 +195,7 @@ __device__ __forceinline__ void merge_row(const Args& a, Piece piece, int np, in
 #pragma unroll
         for (int i = 0; i < N; ++i) e[i] = flip_sign(e[i] * rs, sign_bit(a.signs, lane * N + i));
     }
-    if (store) store_row<N>(a.out, dst + lane * N, e, a.out_dtype);
+    store_row<N>(a.out, dst + lane * N, e, a.out_dtype);
 }
 
 }  // namespace tree

@@ -5,25 +5,47 @@
 // up to 128 query rows); every block takes an equal run of it, so a unit may
 // be cut between blocks, whose pieces the merge kernel joins.
 //
-// A block's tiles alternate between two streams of online softmax over the
-// same query rows, each with its own scores, reference, sum and output
-// accumulator in tensor memory: while one stream's softmax runs, the tensor
-// cores work for the other.  The two are joined at the end of a unit's run,
-// where a row's two accumulators lie in the same tensor-memory lane.
+// A block runs two streams of online softmax, each with its own scores,
+// reference, sum and output accumulator in tensor memory; while one stream's
+// softmax runs, the tensor cores work for the other.  Units of up to 128 rows:
+// the tiles alternate between the streams, which are joined at the end of a
+// unit's run (a row's two accumulators lie in one tensor-memory lane).  Units
+// of up to 256 rows (`pair`): each stream has half of the rows and both read
+// every tile, so a dequantised tile serves twice the rows.  The second row
+// block's queries take the tensor memory of the queries' second fp16 term,
+// so only bf16 outputs, whose rounding (2^-8) hides that of one-term queries
+// (2^-11 of each coordinate), are paired.
 //
 // Roles (20 warps):
-//  * producer (1 warp): bulk copies of packed codes and norms into a ring;
+//  * producer (1 warp): bulk copies of packed codes and norms into a ring (and
+//    2 warps that load the norms where a cache's rows of norms are not 16-byte
+//    aligned);
 //  * dequantisers (8 warps): codes to fp16 operand tiles (128-byte swizzle),
-//    keys as centroids, values as centroids times norms;
-//  * MMA issuer (1 warp): S = (Qhi + Qlo) K~^T (M = 128, N = 64, K = 128) and
-//    O += P V~ (M = 128, N = 128, K = 64), the queries and the weights as A
-//    operands in tensor memory;
-//  * softmax (2 x 4 warps, one query row a thread): scores times key norms,
-//    the tree's mask, lazy online softmax, weights written over the scores.
+//    keys (a tile ahead of values) as centroids, values as centroids times
+//    norms;
+//  * MMA issuer (1 warp): S = (Qhi + Qlo) K~^T (M = 128, N = 64, K = 128) and O += P V~
+//    (M = 128, N = 128, K = 64), the queries and the weights as A operands in
+//    tensor memory;
+//  * softmax (2 x 4 warps, one query row a thread): the queries enter scaled
+//    by the softmax scale (log2 units), so a weight is 2^(S n - reference),
+//    n the key's norm.  There is no pass for the maximum: a row's reference is raised only when
+//    the tile's sum of weights shows that one of them may pass the fp16 range
+//    (always on a stream's first tile), and the tile is then done again.
+//    Weights overwrite the scores.
+//
+// What bounds it is the shared-memory and tensor-memory data path: a tile of
+// 64 keys moves, in 128-byte passes, 256 for the scores, 128 for the weights
+// and 128 for the norms of every 128 rows, and 256 for the operand tiles, 256
+// for the table lookups and 100 for codes once; hence the pairing of row
+// blocks.  (The norm inside K~ would save the norms' passes, but its fp16
+// rounding grows with the scores: 6e-3 of a row's output at score deviations
+// of ten.)
 //
 // Every mbarrier wait is bounded (about a second, then TQ_DEVERR_TIMEOUT; the
 // block stops issuing, waits for its copies and MMAs, frees tensor memory).
 #pragma once
+
+#include <type_traits>
 
 #include "tcgen05.cuh"
 #include "tree_common.cuh"
@@ -35,46 +57,46 @@ namespace mma {
 constexpr int D = 128, BM = 128, BK = 64, NS = 4;
 constexpr int SOFTMAX_WARPS = 8, DEQ_WARPS = 8;
 constexpr int DEQ0 = SOFTMAX_WARPS * 32, LIGHT0 = DEQ0 + DEQ_WARPS * 32;
-constexpr int PRODUCER_WARP = LIGHT0 / 32, MMA_WARP = PRODUCER_WARP + 1;
-constexpr int NTHREADS = LIGHT0 + 128;  // (two idle warps complete the last warpgroup)
-// Registers a thread: launched at 96, the last warpgroup and the
-// dequantisers give up what the softmax warpgroups take:
-// 256 x 152 + 256 x 64 + 128 x 40 <= 640 x 96.
-constexpr int REGS_LAUNCH = 96, REGS_SOFTMAX = 152, REGS_DEQ = 64, REGS_LIGHT = 40;
+constexpr int PRODUCER_WARP = LIGHT0 / 32, MMA_WARP = PRODUCER_WARP + 1, NORM_WARP = MMA_WARP + 1;
+constexpr int NTHREADS = LIGHT0 + 128;
+// Registers a thread: launched at 96, the dequantisers and the last warpgroup
+// give up what the softmax warpgroups take.
+constexpr int REGS_LAUNCH = 96, REGS_SOFTMAX = 136, REGS_DEQ = 64, REGS_LIGHT = 72;
 static_assert(SOFTMAX_WARPS * 32 * REGS_SOFTMAX + DEQ_WARPS * 32 * REGS_DEQ + 128 * REGS_LIGHT <=
                   NTHREADS * REGS_LAUNCH,
               "the register split draws on what the block was launched with");
 // tensor-memory columns (32-bit; fp16 operands take two elements a column)
-constexpr uint32_t TM_QHI = 0, TM_QLO = 64;  // queries / row scale, fp16 [128][128], and their remainder
-constexpr uint32_t TM_S = 128;               // 2 x fp32 scores [128][64]; the weights, fp16, over the first half
-constexpr uint32_t TM_O = 256;               // 2 x fp32 accumulators [128][128]
+constexpr uint32_t TM_Q = 0;     // scaled queries, fp16 [128][128], and their remainder or (pair) the second row block's
+constexpr uint32_t TM_S = 128;   // 2 x fp32 scores [128][64]; the weights, fp16, over their first half
+constexpr uint32_t TM_O = 256;   // 2 x fp32 accumulators [128][128]
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long WAIT_LIMIT = 2000000000ll;  // clock cycles (~1 s)
-constexpr float LAZY = 8.0f;    // log2 headroom before the reference moves
-// weights are 2^(s - reference + WSHIFT) <= 2^14: normal fp16 numbers down to 2^-20 of the reference
-constexpr float WSHIFT = 6.0f;
+// Weights are 2^(s - reference + WSHIFT): 2^6 for a score at the reference,
+// normal fp16 numbers down to 2^-20 of that.  The reference moves when a
+// tile's sum passes WLIMIT, below which no single weight leaves the fp16 range.
+constexpr float WSHIFT = 6.0f, WLIMIT = 32768.0f;
+constexpr float QLIMIT = 60000.0f;  // scaled queries past the fp16 range are cut (their scores pass 10^4 either way)
 
 __host__ __device__ constexpr int row_bytes(int bits) { return bits == 8 ? D : D * bits / 8; }
 // Shared memory (offsets from a 1024-byte aligned base).
 __host__ __device__ constexpr uint32_t lut_bytes(int bits) { return bits == 8 ? 0u : 32u * 4u * (1u << (2 * bits)); }
-// 4-bit key pairs: 256-byte rows, so that a lookup address is one byte
-// permute of the code word (the code byte in bits 8-15, the lane's offset
-// below) and the load's immediate offset holds the table's shared-window
-// address (dynamic shared memory begins at window address SMEM_WINDOW, which
-// the host checks).
+// A lookup address is made of the code word by a shift and one logic
+// operation (the field in bits 7 and up, the lane's offset below), or, for
+// 4-bit keys, whose table has 256-byte rows, by one byte permute; the load's
+// immediate offset holds the table's shared-window address (dynamic shared
+// memory begins at window address SMEM_WINDOW, which the host checks).
 constexpr uint32_t SMEM_WINDOW = 1024;
 __host__ __device__ constexpr bool wide(int kb) { return kb == 4; }
 __host__ __device__ constexpr uint32_t klut_bytes(int kb) { return wide(kb) ? 65536u : lut_bytes(kb); }
 constexpr int SCHED_MAX = 4096;                             // most units the shared schedule holds
 constexpr uint32_t SM_K = 0;                                // 2 x fp16 K~ [64][128]
 constexpr uint32_t SM_V = SM_K + 2 * BK * D * 2;            // 2 x fp16 V~ [64][128]
-constexpr uint32_t SM_KNR = SM_V + 2 * BK * D * 2;          // fp32 key norms of the last four tiles
-constexpr uint32_t SM_AMAX = SM_KNR + 4 * BK * 4;           // float [2][128]: largest |q~| of each half row
-constexpr uint32_t SM_ML = SM_AMAX + 2 * BM * 4;            // float [2][2][128]: a stream's references and sums
+constexpr uint32_t SM_KNR = SM_V + 2 * BK * D * 2;          // fp16 key norms of the last four tiles
+constexpr uint32_t SM_ML = SM_KNR + 4 * BK * 2;             // float [2][2][128]: a stream's references and sums
 constexpr uint32_t SM_CENT = SM_ML + 4 * BM * 4;            // fp16 centroids, keys then values
 constexpr uint32_t SM_BAR = SM_CENT + 64;
 constexpr int B_FULL = 0, B_EMPTY = NS, B_KFULL = 2 * NS, B_KEMPTY = B_KFULL + 2, B_VFULL = B_KEMPTY + 2,
-              B_PV = B_VFULL + 2, B_SFULL = B_PV + 2, B_PFULL = B_SFULL + 2, B_QREADY = B_PFULL + 2,
+              B_VEMPTY = B_VFULL + 2, B_PV = B_VEMPTY + 2, B_SFULL = B_PV + 2, B_PFULL = B_SFULL + 2, B_QREADY = B_PFULL + 2,
               B_FINAL = B_QREADY + 1, NBARS = B_FINAL + 1;
 constexpr uint32_t SM_TMEM = SM_BAR + NBARS * 8;
 constexpr uint32_t SM_FLAG = SM_TMEM + 4;
@@ -124,14 +146,32 @@ __device__ __forceinline__ bool next_segment(const Args& a, const uint8_t* smem,
     return true;
 }
 
+// The same walk tile by tile.
+struct Tiles {
+    int it = -1, gi = -1, j = 0, kend = 0;
+    Segment s{0, 0, 0};
+    __device__ __forceinline__ int keys() const { return min(BK, kend - j * BK); }
+    __device__ __forceinline__ bool next(const Args& a, const uint8_t* smem) {
+        if (++j >= s.j1) {
+            do {
+                if (!next_segment(a, smem, it, s)) return false;
+            } while (s.j1 <= s.j0);
+            j = s.j0;
+            kend = unit_of<BK>(a, s.u).kend;
+        }
+        ++gi;
+        return true;
+    }
+};
+
 // The block whose range holds global tile g (g < total).
 __device__ __forceinline__ int block_of(uint32_t g, uint32_t total, uint32_t nblocks) {
     return static_cast<int>(((static_cast<uint64_t>(g) + 1) * nblocks - 1) / total);
 }
 // A block holds at most two pieces of cut units: the head of the unit its
 // range starts (slot 2c + 1) and a piece of a unit begun earlier (slot 2c).
-// A slot is [BM][D] fp32 rows, then m and l.
-constexpr size_t PART_FLOATS = static_cast<size_t>(BM) * (D + 2);
+// A slot is [rows][D] fp32, then m and l.
+__host__ __device__ constexpr size_t part_floats(int rows) { return static_cast<size_t>(rows) * (D + 2); }
 __device__ __forceinline__ int part_slot(int block, int first_block) { return 2 * block + (block == first_block); }
 
 // --------------------------------------------------------------- dequantise
@@ -154,112 +194,147 @@ __device__ __forceinline__ uint2 int8_to_half(uint32_t b) {
     return make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
 }
 
-// One operand tile [64 slots][128 channels] from a stage's rows: this thread
-// takes channel group dt % 16 (8 channels) of slots dt / 16 + 16 i.  SCALE:
-// times the slot's fp16 norm.  Slots at or past nk are zeros.
-template <int BITS, bool SCALE, bool WIDE>
-__device__ __forceinline__ void dequant_tile(uint32_t tile, uint32_t codes, uint32_t lut, uint32_t snorms,
-                                             const uint16_t* gnorms, bool staged, int dt, int nk) {
-    constexpr int RB = row_bytes(BITS), W = 2 * BITS, IT = BK * (D / 8) / (DEQ_WARPS * 32);
-    constexpr uint32_t M = (1u << W) - 1;
+// Lookup j of a code word through a table with 128-byte rows at TABLE: the
+// field of 2 BITS bits at bit 2 BITS j moves to bit 7.
+template <int BITS, uint32_t TABLE, int J>
+__device__ __forceinline__ uint32_t lookup(uint32_t c, uint32_t l4) {
+    constexpr int SH = 2 * BITS * J - 7;
+    constexpr uint32_t M = ((1u << (2 * BITS)) - 1u) << 7;
+    uint32_t x;
+    if constexpr (SH > 0) x = c >> SH;
+    else x = c << -SH;
+    return ptx::lds32_imm<TABLE>((x & M) | l4);
+}
+
+// One operand tile [64 slots][128 channels] from a stage's rows by THREADS
+// threads: this one takes channel group dt % 16 (8 channels) of slots
+// dt / 16 + (THREADS / 16) i.  SCALE: times the slot's fp16 norm.  Slots at or
+// past nk are zeros.
+template <int BITS, bool SCALE, bool WIDE, uint32_t TABLE, int THREADS>
+__device__ __forceinline__ void dequant_tile(uint32_t tile, uint32_t codes, uint32_t snorms, int dt, int nk) {
+    constexpr int RB = row_bytes(BITS), IT = BK * (D / 8) / THREADS, KS = THREADS / 16, B = 4;
+    static_assert(IT % B == 0, "whole batches");
     const int cg = dt & 15, k0 = dt >> 4;
-    uint4 v[IT];
-    if constexpr (BITS == 8) {
+    const uint32_t l4 = 4u * static_cast<uint32_t>(dt & 31);
+    // (in batches of four slots, whose loads go out together)
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const uint32_t at = codes + (k0 + 16 * i) * RB + 8 * cg;
-            const uint2 p = int8_to_half(ptx::lds32(at)), q = int8_to_half(ptx::lds32(at + 4));
-            v[i] = make_uint4(p.x, p.y, q.x, q.y);
-        }
-    } else {
-        uint32_t c8[IT];
+    for (int b = 0; b < IT; b += B) {
+        uint4 v[B];
+        if constexpr (BITS == 8) {
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const uint32_t row = codes + (k0 + 16 * i) * RB;
-            if constexpr (BITS == 4) {
-                c8[i] = ptx::lds32(row + 4 * cg);
-            } else if constexpr (BITS == 2) {
-                c8[i] = ptx::lds16(row + 2 * cg);
-            } else {  // 24 bits from bit 24 cg: may straddle two words
-                const int bit = 24 * cg, w = bit >> 5, sh = bit & 31;
-                const uint32_t lo = ptx::lds32(row + 4 * w), hi = ptx::lds32(row + 4 * min(w + 1, RB / 4 - 1));
-                c8[i] = __funnelshift_r(lo, hi, sh);
-            }
-        }
-        if constexpr (WIDE) {
-            const uint32_t l4 = 4u * static_cast<uint32_t>(dt & 31);
-            constexpr uint32_t T = SMEM_WINDOW + SM_KLUT;
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                v[i].x = ptx::lds32_imm<T>(__byte_perm(c8[i], l4, 0x7604));
-                v[i].y = ptx::lds32_imm<T>(__byte_perm(c8[i], l4, 0x7614));
-                v[i].z = ptx::lds32_imm<T>(__byte_perm(c8[i], l4, 0x7624));
-                v[i].w = ptx::lds32_imm<T>(__byte_perm(c8[i], l4, 0x7634));
+            for (int i = 0; i < B; ++i) {
+                const uint32_t at = codes + (k0 + KS * (b + i)) * RB + 8 * cg;
+                const uint2 p = int8_to_half(ptx::lds32(at)), q = int8_to_half(ptx::lds32(at + 4));
+                v[i] = make_uint4(p.x, p.y, q.x, q.y);
             }
         } else {
+            uint32_t c8[B];
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                v[i].x = ptx::lds32(lut + 128u * (c8[i] & M));
-                v[i].y = ptx::lds32(lut + 128u * ((c8[i] >> W) & M));
-                v[i].z = ptx::lds32(lut + 128u * ((c8[i] >> (2 * W)) & M));
-                v[i].w = ptx::lds32(lut + 128u * ((c8[i] >> (3 * W)) & M));
+            for (int i = 0; i < B; ++i) {
+                const uint32_t row = codes + (k0 + KS * (b + i)) * RB;
+                if constexpr (BITS == 4) {
+                    c8[i] = ptx::lds32(row + 4 * cg);
+                } else if constexpr (BITS == 2) {
+                    c8[i] = ptx::lds16(row + 2 * cg);
+                } else {  // 24 bits from bit 24 cg: may straddle two words
+                    const int bit = 24 * cg, w = bit >> 5, sh = bit & 31;
+                    const uint32_t lo = ptx::lds32(row + 4 * w), hi = ptx::lds32(row + 4 * min(w + 1, RB / 4 - 1));
+                    c8[i] = __funnelshift_r(lo, hi, sh);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if constexpr (WIDE) {
+                    v[i].x = ptx::lds32_imm<TABLE>(__byte_perm(c8[i], l4, 0x7604));
+                    v[i].y = ptx::lds32_imm<TABLE>(__byte_perm(c8[i], l4, 0x7614));
+                    v[i].z = ptx::lds32_imm<TABLE>(__byte_perm(c8[i], l4, 0x7624));
+                    v[i].w = ptx::lds32_imm<TABLE>(__byte_perm(c8[i], l4, 0x7634));
+                } else {
+                    v[i].x = lookup<BITS, TABLE, 0>(c8[i], l4);
+                    v[i].y = lookup<BITS, TABLE, 1>(c8[i], l4);
+                    v[i].z = lookup<BITS, TABLE, 2>(c8[i], l4);
+                    v[i].w = lookup<BITS, TABLE, 3>(c8[i], l4);
+                }
             }
         }
-    }
-    if constexpr (SCALE) {
+        if constexpr (SCALE) {
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int key = k0 + 16 * i;
-            uint32_t nb = staged ? ptx::lds16(snorms + 2 * key) : (key < nk ? gnorms[key] : uint16_t(0));
-            // (a norm that is not finite: the row is zeros, its key's score NaN)
-            if ((nb & 0x7C00u) == 0x7C00u) nb = 0u;
-            const uint32_t n2 = nb | (nb << 16);
-            const __half2 f = *reinterpret_cast<const __half2*>(&n2);
-            __half2* h = reinterpret_cast<__half2*>(&v[i]);
+            for (int i = 0; i < B; ++i) {
+                uint32_t nb = ptx::lds16(snorms + 2 * (k0 + KS * (b + i)));
+                // (a norm that is not finite: the row is zeros, its key's score NaN)
+                if ((nb & 0x7C00u) == 0x7C00u) nb = 0u;
+                const uint32_t n2 = nb | (nb << 16);
+                const __half2 f = *reinterpret_cast<const __half2*>(&n2);
+                __half2* h = reinterpret_cast<__half2*>(&v[i]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
+                for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
+            }
         }
-    }
-    if (nk < BK) {  // the last, partial tile only
+        if (nk < BK) {  // the last, partial tile only
 #pragma unroll
-        for (int i = 0; i < IT; ++i)
-            if (k0 + 16 * i >= nk) v[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
+            for (int i = 0; i < B; ++i)
+                if (k0 + KS * (b + i) >= nk) v[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-    for (int i = 0; i < IT; ++i) ptx::sts128(tile + tc::sw128_offset(k0 + 16 * i, 8 * cg, BK), v[i]);
+        for (int i = 0; i < B; ++i) ptx::sts128(tile + tc::sw128_offset(k0 + KS * (b + i), 8 * cg, BK), v[i]);
+    }
+}
+
+__device__ __forceinline__ float2 half2_float2(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
 // Walsh-Hadamard butterflies over 64 values.
 __device__ __forceinline__ void fwht64(float (&x)[64]) { fwht_registers(x); }
 
 // This half's 64 values of a query row after the first butterfly stage
-// (x[i] +- x[i + 64], signs applied), or (int8 keys) the half itself.
-__device__ __forceinline__ void load_half(const Args& a, size_t off, int half, bool rotate, float (&x)[64]) {
-    if (!rotate) {
+// (x[i] +- x[i + 64], signs applied), or (int8 keys) the half itself.  Four
+// 16-byte loads are in flight at a time.
+template <int DTYPE, bool ROTATE>
+__device__ __forceinline__ void load_half_typed(const Args& a, size_t off, int half, float (&x)[64]) {
+    constexpr int E = DTYPE == 0 ? 4 : 8;  // elements of a 16-byte load
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + off * (DTYPE == 0 ? 4 : 2));
+    auto value = [](const uint4& w, int e) -> float {
+        const uint32_t u = DTYPE == 0 ? (e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w)
+                                      : (e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w);
+        if (DTYPE == 0) return __uint_as_float(u);
+        if (DTYPE == 1) return __uint_as_float((e & 1) ? u & 0xffff0000u : u << 16);
+        const __half2 h = *reinterpret_cast<const __half2*>(&u);
+        return (e & 1) ? __high2float(h) : __low2float(h);
+    };
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-            float v[4];
-            load4(a.q, off + 64 * half + c, a.q_dtype, v);
+    for (int c = 0; c < 64; c += 2 * E) {
+        uint4 lo[2], hi[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[c + e] = v[e];
-            if (c % 16 == 12) asm volatile("" ::: "memory");
+        for (int i = 0; i < 2; ++i) {
+            if (ROTATE) {
+                lo[i] = p[c / E + i];
+                hi[i] = p[64 / E + c / E + i];
+            } else {
+                lo[i] = p[(64 / E) * half + c / E + i];
+            }
         }
-        return;
-    }
 #pragma unroll
-    for (int c = 0; c < 64; c += 4) {
-        float lo[4], hi[4];
-        load4(a.q, off + c, a.q_dtype, lo);
-        load4(a.q, off + 64 + c, a.q_dtype, hi);
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float p = flip_sign(lo[e], (a.signs[(c + e) >> 5] >> ((c + e) & 31)) & 1u);
-            const float q = flip_sign(hi[e], (a.signs[2 + ((c + e) >> 5)] >> ((c + e) & 31)) & 1u);
-            x[c + e] = half ? p - q : p + q;
-        }
-        // (a few loads in flight at a time: all of them together would not fit the registers)
-        if (c % 16 == 12) asm volatile("" ::: "memory");
+            for (int e = 0; e < E; ++e) {
+                const int k = c + E * i + e;
+                if (ROTATE) {
+                    const float u = flip_sign(value(lo[i], e), (a.signs[k >> 5] >> (k & 31)) & 1u);
+                    const float v = flip_sign(value(hi[i], e), (a.signs[2 + (k >> 5)] >> (k & 31)) & 1u);
+                    x[k] = half ? u - v : u + v;
+                } else {
+                    x[k] = value(lo[i], e);
+                }
+            }
+        asm volatile("" ::: "memory");
     }
+}
+template <bool ROTATE>
+__device__ __forceinline__ void load_half(const Args& a, size_t off, int half, float (&x)[64]) {
+    if (a.q_dtype == TQ_BF16) load_half_typed<1, ROTATE>(a, off, half, x);
+    else if (a.q_dtype == TQ_F16) load_half_typed<2, ROTATE>(a, off, half, x);
+    else load_half_typed<0, ROTATE>(a, off, half, x);
 }
 
 // 8 consecutive fp32 columns of this thread's tensor-memory lane.
@@ -295,23 +370,27 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
         return true;
     };
     const int G = a.group;
-    // softmax warps of a stream that own query rows
-    const int aw = (min(BM, min(a.tok_per_tile, a.n_draft) * G) + 31) / 32;
+    const bool pair = a.pair;
+    // softmax warps that own query rows, of each stream
+    const int rows = a.tok_per_tile * G;
+    const int aw0 = (min(BM, rows) + 31) / 32, aw1 = pair ? (rows - BM + 31) / 32 : aw0;
+    const int soft_threads = 32 * (aw0 + aw1);
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            ptx::mbar_init(bar(B_FULL + i), 1);
+            ptx::mbar_init(bar(B_FULL + i), a.staged_norms ? 1 : 2);
             ptx::mbar_init(bar(B_EMPTY + i), DEQ_WARPS);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(B_KFULL + i), DEQ_WARPS);
             ptx::mbar_init(bar(B_KEMPTY + i), 1);
             ptx::mbar_init(bar(B_VFULL + i), DEQ_WARPS);
+            ptx::mbar_init(bar(B_VEMPTY + i), 1);
             ptx::mbar_init(bar(B_PV + i), 1);
             ptx::mbar_init(bar(B_SFULL + i), 1);
-            ptx::mbar_init(bar(B_PFULL + i), aw);
+            ptx::mbar_init(bar(B_PFULL + i), i ? aw1 : aw0);
         }
-        ptx::mbar_init(bar(B_QREADY), 2 * aw);
+        ptx::mbar_init(bar(B_QREADY), aw0 + aw1);
         ptx::mbar_init(bar(B_FINAL), 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -323,11 +402,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
     }
     __syncthreads();
     if (warp >= DEQ0 / 32 && warp < LIGHT0 / 32) {
+        constexpr int N = LIGHT0 - DEQ0;
         const uint16_t* kcent = reinterpret_cast<const uint16_t*>(smem + SM_CENT);
-        if constexpr (KB < 8)
-            build_lut<KB, wide(KB) ? 64 : 32>(reinterpret_cast<uint32_t*>(smem + SM_KLUT), kcent, tid - DEQ0, DEQ_WARPS * 32);
-        if constexpr (VB < 8)
-            build_lut<VB>(reinterpret_cast<uint32_t*>(smem + sm_vlut(KB)), kcent + 16, tid - DEQ0, DEQ_WARPS * 32);
+        if constexpr (KB < 8) build_lut<KB, wide(KB) ? 64 : 32>(reinterpret_cast<uint32_t*>(smem + SM_KLUT), kcent, tid - DEQ0, N);
+        if constexpr (VB < 8) build_lut<VB>(reinterpret_cast<uint32_t*>(smem + sm_vlut(KB)), kcent + 16, tid - DEQ0, N);
     }
     // everything above overlaps the end of the kernel before; nothing of the
     // caller's memory has been read or written yet
@@ -409,7 +487,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
     constexpr uint32_t ST_VC = BK * kbytes, ST_KN = ST_VC + BK * vbytes, ST_VN = ST_KN + BK * 2;
 
     // Every role walks the same segments; tile gi (counted over the block's
-    // run) is in ring stage gi % NS and belongs to stream gi % 2.
+    // run) is in ring stage gi % NS and operand buffers gi % 2.  A stream's
+    // steps are its tiles: all of them (pair), or tile gi is step gi / 2 of
+    // stream gi % 2.
     if (warp >= LIGHT0 / 32) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LIGHT));
         if (warp == PRODUCER_WARP) {
@@ -453,27 +533,78 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
             // every copy issued must land before the block may exit
             for (int k = max(0, gi - NS); k < gi; ++k)
                 ptx::mbar_wait_bounded(bar(B_FULL + k % NS), (k / NS) & 1, WAIT_LIMIT);
+        } else if (warp >= NORM_WARP) {
+            // ---------------------------------------- norms that are not staged
+            if (!a.staged_norms) {
+                int gi = 0, it = -1;
+                Segment s;
+                while (next_segment(a, smem, it, s)) {
+                    const Unit x = unit_of<BK>(a, s.u);
+                    const size_t row0 = (static_cast<size_t>(x.b) * a.hkv + x.kv) * a.capacity;
+                    for (int j = s.j0; j < s.j1; ++j, ++gi) {
+                        if ((gi & 1) != warp - NORM_WARP) continue;
+                        const int st = gi % NS, nk = min(BK, x.kend - j * BK);
+                        const size_t row = row0 + static_cast<size_t>(j) * BK;
+                        uint16_t n[4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int k = lane + 32 * h;
+                            n[h] = k < nk ? a.k_norms[row + k] : uint16_t(0);
+                            n[2 + h] = k < nk ? a.v_norms[row + k] : uint16_t(0);
+                        }
+                        if (gi >= NS && !wait(B_EMPTY + st, ((gi - NS) / NS) & 1)) goto norms_done;
+                        uint16_t* kn = reinterpret_cast<uint16_t*>(smem + STAGE + st * STAGE_BYTES + ST_KN);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            kn[lane + 32 * h] = n[h];
+                            kn[BK + lane + 32 * h] = n[2 + h];
+                        }
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bar(B_FULL + st));
+                    }
+                }
+            }
+        norms_done:;
         } else if (warp == MMA_WARP) {
             // ----------------------------------------------------- MMA issuer
             const bool leader = tc::elect_one();
             const uint32_t idesc_s = tc::idesc_f16(BM, BK), idesc_o = tc::idesc_f16_bmn(BM, D);
             const uint64_t kdesc0 = tc::sw128_desc(sbase + SM_K);
             const uint64_t vdesc0 = tc::sw128_mn_desc(sbase + SM_V, BK * 128, 1024);
-            auto issue_s = [&](int gi) -> bool {
+            // scores of stream g from tile gi; the tile's last reader frees it
+            auto issue_s = [&](int gi, int g, bool last) -> bool {
                 const int bf = gi & 1;
                 if (!wait(B_KFULL + bf, (gi >> 1) & 1)) return false;
                 tc::fence_after_sync();
                 if (leader) {
                     const uint64_t kd = kdesc0 + static_cast<uint64_t>(bf * (BK * D * 2) >> 4);
-                    const uint32_t sd = tmem + TM_S + BK * bf;
+                    const uint32_t sd = tmem + TM_S + BK * g, qd = tmem + TM_Q + (pair ? 64 * g : 0);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         const uint64_t bd = kd + static_cast<uint64_t>(((ks >> 2) * (BK * 128) + (ks & 3) * 32) >> 4);
-                        tc::mma_f16_ts(sd, tmem + TM_QHI + 8 * ks, bd, idesc_s, ks > 0);
-                        tc::mma_f16_ts(sd, tmem + TM_QLO + 8 * ks, bd, idesc_s, true);
+                        tc::mma_f16_ts(sd, qd + 8 * ks, bd, idesc_s, ks > 0);
+                        if (!pair) tc::mma_f16_ts(sd, qd + 64 + 8 * ks, bd, idesc_s, true);
                     }
-                    tc::commit(bar(B_SFULL + bf));
-                    tc::commit(bar(B_KEMPTY + bf));
+                    tc::commit(bar(B_SFULL + g));
+                    if (last) tc::commit(bar(B_KEMPTY + bf));
+                }
+                __syncwarp();
+                return true;
+            };
+            // output of stream g's step q from tile gi
+            auto issue_pv = [&](int gi, int g, int q, bool first, bool last) -> bool {
+                const int bf = gi & 1;
+                if (!wait(B_PFULL + g, q & 1)) return false;
+                if (!wait(B_VFULL + bf, (gi >> 1) & 1)) return false;
+                tc::fence_after_sync();
+                if (leader) {
+                    const uint64_t vd = vdesc0 + static_cast<uint64_t>(bf * (BK * D * 2) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < BK / 16; ++ks)
+                        tc::mma_f16_ts(tmem + TM_O + D * g, tmem + TM_S + BK * g + 8 * ks,
+                                       vd + static_cast<uint64_t>(ks * 2048 >> 4), idesc_o, !first || ks > 0);
+                    tc::commit(bar(B_PV + g));
+                    if (last) tc::commit(bar(B_VEMPTY + bf));
                 }
                 __syncwarp();
                 return true;
@@ -486,27 +617,30 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 if (!wait(B_QREADY, qs & 1)) break;
                 ++qs;
                 const int gfirst = gi, gend = gi + (s.j1 - s.j0);
-                if (!issue_s(gi)) break;
-                if (gi + 1 < gend && !issue_s(gi + 1)) break;
-                for (; gi < gend; ++gi) {
-                    const int bf = gi & 1;
-                    if (!wait(B_PFULL + bf, (gi >> 1) & 1)) goto issued;
-                    if (!wait(B_VFULL + bf, (gi >> 1) & 1)) goto issued;
-                    tc::fence_after_sync();
-                    if (leader) {
-                        const uint64_t vd = vdesc0 + static_cast<uint64_t>(bf * (BK * D * 2) >> 4);
-                        const uint32_t pa = tmem + TM_S + BK * bf;
-#pragma unroll
-                        for (int ks = 0; ks < BK / 16; ++ks)
-                            tc::mma_f16_ts(tmem + TM_O + D * bf, pa + 8 * ks, vd + static_cast<uint64_t>(ks * 2048 >> 4),
-                                           idesc_o, gi >= gfirst + 2 || ks > 0);
-                        tc::commit(bar(B_PV + bf));
+                // (a stream's weights lie in its score buffer: its P V is
+                // waited for before the buffer is written again)
+                if (pair) {
+                    if (!issue_s(gi, 0, false) || !issue_s(gi, 1, true)) break;
+                    for (; gi < gend; ++gi) {
+#pragma unroll 1
+                        for (int g = 0; g < 2; ++g) {
+                            if (!issue_pv(gi, g, gi, gi == gfirst, g == 1)) goto issued;
+                            if (gi + 1 < gend) {
+                                if (!wait(B_PV + g, gi & 1)) goto issued;
+                                if (!issue_s(gi + 1, g, g == 1)) goto issued;
+                            }
+                        }
                     }
-                    __syncwarp();
-                    if (gi + 2 < gend) {
-                        // the stream's weights lie in its score buffer: they are used before it is written again
-                        if (!wait(B_PV + bf, (gi >> 1) & 1)) goto issued;
-                        if (!issue_s(gi + 2)) goto issued;
+                } else {
+                    if (!issue_s(gi, gi & 1, true)) break;
+                    if (gi + 1 < gend && !issue_s(gi + 1, (gi + 1) & 1, true)) break;
+                    for (; gi < gend; ++gi) {
+                        const int g = gi & 1, q = gi >> 1;
+                        if (!issue_pv(gi, g, q, gi < gfirst + 2, true)) goto issued;
+                        if (gi + 2 < gend) {
+                            if (!wait(B_PV + g, q & 1)) goto issued;
+                            if (!issue_s(gi + 2, g, true)) goto issued;
+                        }
                     }
                 }
             }
@@ -521,35 +655,36 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
         // ------------------------------------------------------ dequantisers
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DEQ));
         const int dt = tid - DEQ0;
-        const uint32_t klane = sbase + SM_KLUT + 4 * lane, vlane = sbase + sm_vlut(KB) + 4 * lane;
-        int gi = 0, it = -1;
-        Segment s;
-        while (next_segment(a, smem, it, s)) {
-            const Unit x = unit_of<BK>(a, s.u);
-            const size_t row0 = (static_cast<size_t>(x.b) * a.hkv + x.kv) * a.capacity;  // (norms that are not staged)
-            for (int j = s.j0; j < s.j1; ++j, ++gi) {
-                const int st = gi % NS, bf = gi & 1, nk = min(BK, x.kend - j * BK);
-                if (!wait(B_FULL + st, (gi / NS) & 1)) goto dequantised;
+        // (keys run a tile ahead of values: K~(gi + 1) waits for the scores of
+        // tile gi - 1 only, V~(gi) for the P V of tile gi - 2)
+        Tiles k, v;
+        for (;;) {
+            const bool more = k.next(a, smem);
+            if (more) {
+                const int gi = k.gi, st = gi % NS, bf = gi & 1, nk = k.keys();
                 const uint32_t sst = sbase + STAGE + st * STAGE_BYTES;
-                const size_t row = row0 + static_cast<size_t>(j) * BK;
+                if (!wait(B_FULL + st, (gi / NS) & 1)) goto dequantised;
                 if (gi >= 2 && !wait(B_KEMPTY + bf, ((gi - 2) >> 1) & 1)) goto dequantised;
-                // the tile's key norms, for the softmax (the softmax of tile gi - 4 is done: S(gi - 2) followed it)
                 if (dt < BK) {
-                    uint16_t kn = 0, vn = 0;
-                    if (dt < nk) {
-                        kn = a.staged_norms ? ptx::lds16(sst + ST_KN + 2 * dt) : a.k_norms[row + dt];
-                        vn = a.staged_norms ? ptx::lds16(sst + ST_VN + 2 * dt) : a.v_norms[row + dt];
-                    }
-                    reinterpret_cast<float*>(smem + SM_KNR)[(gi & 3) * BK + dt] =
-                        (vn & 0x7C00u) == 0x7C00u ? NAN : half_bits_to_float(kn);
+                    // the tile's key norms, for the softmax (which is through
+                    // with tile gi - 4: the scores of tile gi - 2 followed it)
+                    const uint16_t kn = ptx::lds16(sst + ST_KN + 2 * dt), vn = ptx::lds16(sst + ST_VN + 2 * dt);
+                    reinterpret_cast<uint16_t*>(smem + SM_KNR)[(gi & 3) * BK + dt] =
+                        dt >= nk ? uint16_t(0) : (vn & 0x7C00u) == 0x7C00u ? uint16_t(0x7E00) : kn;
                 }
-                dequant_tile<KB, false, wide(KB)>(sbase + SM_K + bf * (BK * D * 2), sst, klane, 0u, nullptr, true, dt, nk);
+                dequant_tile<KB, false, wide(KB), SMEM_WINDOW + SM_KLUT, DEQ_WARPS * 32>(
+                    sbase + SM_K + bf * (BK * D * 2), sst, 0u, dt, nk);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(B_KFULL + bf));
-                if (gi >= 2 && !wait(B_PV + bf, ((gi - 2) >> 1) & 1)) goto dequantised;
-                dequant_tile<VB, true, false>(sbase + SM_V + bf * (BK * D * 2), sst + ST_VC, vlane, sst + ST_VN,
-                                              a.v_norms + row, a.staged_norms != 0, dt, nk);
+            }
+            if (v.gi < (more ? k.gi - 1 : k.gi)) {
+                v.next(a, smem);
+                const int gi = v.gi, st = gi % NS, bf = gi & 1;
+                const uint32_t sst = sbase + STAGE + st * STAGE_BYTES;
+                if (gi >= 2 && !wait(B_VEMPTY + bf, ((gi - 2) >> 1) & 1)) goto dequantised;
+                dequant_tile<VB, true, false, SMEM_WINDOW + sm_vlut(KB), DEQ_WARPS * 32>(
+                    sbase + SM_V + bf * (BK * D * 2), sst + ST_VC, sst + ST_VN, dt, v.keys());
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -557,128 +692,149 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     ptx::mbar_arrive(bar(B_EMPTY + st));
                 }
             }
+            if (!more) break;
         }
     dequantised:;
     } else {
         // ---------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
-        const int g = warp >> 2, r = tid & 127;  // stream, query row
-        const int rt = r / G, rh = r % G;
+        const int g = warp >> 2, r = tid & 127;  // stream, its tensor-memory lane
+        const int ur = pair ? BM * g + r : r;    // query row of the unit
+        const int rt = ur / G, rh = ur % G;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         constexpr float rsqrt_d = 0.08838834764831845f;
-        float* amax = reinterpret_cast<float*>(smem + SM_AMAX);
         float* ml = reinterpret_cast<float*>(smem + SM_ML);
         int gi = 0, it = -1;
         Segment s;
-        if ((warp & 3) >= aw) it = U;  // no rows: the warp takes no part
+        if ((warp & 3) >= (g ? aw1 : aw0)) it = U;  // no rows: the warp takes no part
         while (next_segment(a, smem, it, s)) {
             const Unit x = unit_of<BK>(a, s.u);
-            const bool row_ok = rt < x.ntok && rt * G + rh < BM;
+            const bool row_ok = rt < x.ntok;
             const size_t qoff = ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + rt) * a.hq + x.kv * G + rh) * D;
+            // this thread's 64-channel halves of the row: both, or (two streams over the same rows) its stream's
+            const int h0 = pair ? 0 : g, h1 = pair ? 2 : g + 1;
             if (s.j1 <= s.j0) {
                 // no tiles: a refused sequence, or one without drafts in this unit
                 if (x.bad) {
                     if (x.qt == 0 && x.kv == 0 && tid == 0 && a.err) atomicOr(a.err, TQ_DEVERR_SEQLEN);
-                    if (rt < min(a.tok_per_tile, a.n_draft - x.tok0) && rt * G + rh < BM) {
+                    if (rt < min(a.tok_per_tile, a.n_draft - x.tok0)) {
                         const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-                        for (int c = 0; c < 64; c += 8) store_row<8>(a.out, qoff + 64 * g + c, z, a.out_dtype);
+                        for (int c = 64 * h0; c < 64 * h1; c += 8) store_row<8>(a.out, qoff + c, z, a.out_dtype);
                     }
                 }
                 continue;
             }
-            float qscale;
-            {
-                // ---- this stream's half of the row's queries
+            // ---- the row's queries, in log2 units of the score per unit of the key
+#pragma unroll 1
+            for (int h = h0; h < h1; ++h) {
                 float q[64];
                 if (row_ok) {
-                    load_half(a, qoff, g, KB < 8, q);
+                    load_half<(KB < 8)>(a, qoff, h, q);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 64; ++i) q[i] = 0.f;
                 }
                 __syncwarp();
                 if constexpr (KB < 8) fwht64(q);
-                float m = 0.f;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(q[i]));
-                amax[g * BM + r] = m;
-                // (after a wait that ran out every softmax warp leaves at the
-                // same barrier)
-                if (ptx::named_barrier_or(2, 2 * aw * 32, *abort_flag != 0)) goto softmax_done;
-                m = fmaxf(m, amax[(1 - g) * BM + r]);
-                qscale = KB < 8 ? m * rsqrt_d : m;
-                const float inv = m > 0.f ? 1.f / m : 0.f;
+                const float scale = KB < 8 ? a.score_scale * rsqrt_d : a.score_scale;
 #pragma unroll
                 for (int c = 0; c < 64; c += 16) {
                     uint32_t hw[8], lw[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float v0 = q[c + 2 * e] * inv, v1 = q[c + 2 * e + 1] * inv;
-                        const __half h0 = __float2half_rn(v0), h1 = __float2half_rn(v1);
-                        hw[e] = pack2(__half_as_ushort(h0), __half_as_ushort(h1));
-                        lw[e] = ptx::pack_half2(v0 - __half2float(h0), v1 - __half2float(h1));
+                        float v0 = q[c + 2 * e] * scale, v1 = q[c + 2 * e + 1] * scale;
+                        if (fabsf(v0) > QLIMIT) v0 = copysignf(QLIMIT, v0);  // (NaN stays)
+                        if (fabsf(v1) > QLIMIT) v1 = copysignf(QLIMIT, v1);
+                        hw[e] = ptx::pack_half2(v0, v1);
+                        const float2 hf = half2_float2(hw[e]);
+                        lw[e] = ptx::pack_half2(v0 - hf.x, v1 - hf.y);
                     }
-                    tc::st_8cols(tmem + lanes + TM_QHI + 32 * g + c / 2, hw);
-                    tc::st_8cols(tmem + lanes + TM_QLO + 32 * g + c / 2, lw);
+                    tc::st_8cols(tmem + lanes + TM_Q + (pair ? 64 * g : 0) + 32 * h + c / 2, hw);
+                    if (!pair) tc::st_8cols(tmem + lanes + TM_Q + 64 + 32 * h + c / 2, lw);
                 }
             }
             tc::st_wait();
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(B_QREADY));
-            const float rs = fmaxf(qscale * a.score_scale, 1e-30f);  // (keeps a masked -inf score -inf)
             const uint64_t mask = row_ok ? row_mask(a, x, x.tok0 + rt) : 0ull;
             float mref = NOTHING, l = 0.f;
-            bool dead = false;
-            const int gfirst = gi, gend = gi + (s.j1 - s.j0);
-            gi += (gi & 1) != g;  // the stream's first tile of the segment
-            for (; gi < gend; gi += 2) {
-                dead = !wait(B_SFULL + g, (gi >> 1) & 1);
+            bool dead = false, first = true;
+            const int gfirst = gi, gend = gi + (s.j1 - s.j0), inc = pair ? 1 : 2;
+            if (!pair) gi += (gi & 1) != g;  // the stream's first tile of the segment
+            for (; gi < gend; gi += inc, first = false) {
+                const int q = pair ? gi : gi >> 1;
+                dead = !wait(B_SFULL + g, q & 1);
                 if (dead) break;
                 tc::fence_after_sync();
-                float sc[BK];
-                {
-                    float (&sc0)[32] = *reinterpret_cast<float (*)[32]>(&sc[0]);
-                    float (&sc1)[32] = *reinterpret_cast<float (*)[32]>(&sc[32]);
-                    tc::ld_32cols(tmem + lanes + TM_S + BK * g, sc0);
-                    tc::ld_32cols(tmem + lanes + TM_S + BK * g + 32, sc1);
-                }
-                tc::ld_wait();
-                const float4* kn4 = reinterpret_cast<const float4*>(smem + SM_KNR + (gi & 3) * BK * 4);
-#pragma unroll
-                for (int i = 0; i < BK; i += 4) {
-                    const float4 k4 = kn4[i / 4];
-                    const float2 a01 = ptx::fmul2(make_float2(sc[i], sc[i + 1]), make_float2(k4.x, k4.y));
-                    const float2 a23 = ptx::fmul2(make_float2(sc[i + 2], sc[i + 3]), make_float2(k4.z, k4.w));
-                    sc[i] = a01.x;
-                    sc[i + 1] = a01.y;
-                    sc[i + 2] = a23.x;
-                    sc[i + 3] = a23.y;
-                }
+                const uint32_t kn = sbase + SM_KNR + (gi & 3) * BK * 2;
                 const int key0 = (s.j0 + gi - gfirst) * BK;
-                if (key0 + BK > x.base) {  // a tile with drafts: the tree's mask
+                const bool masked = key0 + BK > x.base;  // a tile with drafts: the tree's mask
+                uint32_t vis[2] = {0u, 0u};
+                if (masked) {
                     const uint64_t v = visible(mask, key0, x.base);
-                    const uint32_t v0 = static_cast<uint32_t>(v), v1 = static_cast<uint32_t>(v >> 32);
-#pragma unroll
-                    for (int i = 0; i < BK; ++i)
-                        if (!(((i < 32 ? v0 : v1) >> (i & 31)) & 1u)) sc[i] = -INFINITY;
+                    vis[0] = static_cast<uint32_t>(v);
+                    vis[1] = static_cast<uint32_t>(v >> 32);
                 }
-                float m4[4];
+                uint32_t pw[BK / 2];
+                float sum;
+                // the tile's weights against the present reference, and their
+                // sum (one straight run of code without the mask's test)
+                auto weigh = [&](auto with_mask) {
+                    const float2 nm2 = make_float2(WSHIFT - mref, WSHIFT - mref);
+                    float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+                    float sc[32];
+                    uint4 k8;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float m = sc[16 * q];
+                    for (int i = 0; i < BK; i += 4) {
+                        if (i % 32 == 0) {
+                            tc::ld_32cols(tmem + lanes + TM_S + BK * g + i, sc);
+                            tc::ld_wait();
+                        }
+                        if (i % 8 == 0) k8 = ptx::lds128(kn + 2 * i);  // the norms of 8 keys
+                        const int e = i % 32;
+                        const float2 n0 = half2_float2(i % 8 ? k8.z : k8.x), n1 = half2_float2(i % 8 ? k8.w : k8.y);
+                        float2 t0 = ptx::ffma2(make_float2(sc[e], sc[e + 1]), n0, nm2);
+                        float2 t1 = ptx::ffma2(make_float2(sc[e + 2], sc[e + 3]), n1, nm2);
+                        if constexpr (decltype(with_mask)::value) {
+                            const uint32_t v = vis[i / 32] >> e;
+                            if (!(v & 1u)) t0.x = -INFINITY;
+                            if (!(v & 2u)) t0.y = -INFINITY;
+                            if (!(v & 4u)) t1.x = -INFINITY;
+                            if (!(v & 8u)) t1.y = -INFINITY;
+                        }
+                        const float2 p0 = make_float2(ptx::ex2(t0.x), ptx::ex2(t0.y));
+                        const float2 p1 = make_float2(ptx::ex2(t1.x), ptx::ex2(t1.y));
+                        acc0 = ptx::fadd2(acc0, p0);
+                        acc1 = ptx::fadd2(acc1, p1);
+                        pw[i / 2] = ptx::pack_half2(p0.x, p0.y);
+                        pw[i / 2 + 1] = ptx::pack_half2(p1.x, p1.y);
+                    }
+                    sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                };
+#pragma unroll 1
+                for (bool again = false;; again = true) {
+                    if (masked) weigh(std::true_type());
+                    else weigh(std::false_type());
+                    if (again || !__any_sync(kFullMask, !(sum <= WLIMIT))) break;
+                    // a weight may leave the fp16 range (or is NaN): raise the
+                    // reference to the row's largest score, rescale, again
+                    float m = -INFINITY;
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {
+                        float sc[16];
+                        tc::ld_16cols(tmem + lanes + TM_S + BK * g + 16 * h, sc);
+                        tc::ld_wait();
+                        const uint32_t v = masked ? (h < 2 ? vis[0] : vis[1]) >> (16 * (h & 1)) : ~0u;
 #pragma unroll
-                    for (int i = 1; i < 15; i += 2) m = ptx::fmax3(m, sc[16 * q + i], sc[16 * q + i + 1]);
-                    m4[q] = fmaxf(m, sc[16 * q + 15]);
-                }
-                const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rs;
-                const bool need = mt > mref + LAZY;
-                if (__any_sync(kFullMask, need)) {
-                    const float mnew = need ? mt : mref;
-                    const float c = ptx::ex2(mref - mnew);
-                    if (gi >= gfirst + 2) {
-                        // (scores of this tile came after the stream's last P V: its accumulator is complete)
+                        for (int i = 0; i < 16; ++i) {
+                            const float n = half_bits_to_float(ptx::lds16(kn + 2 * (16 * h + i)));
+                            if ((v >> i) & 1u) m = fmaxf(m, sc[i] * n);
+                        }
+                    }
+                    const float mnew = fmaxf(m, mref), c = ptx::ex2(mref - mnew);
+                    if (!first) {  // (this step's scores came after the stream's last P V: the accumulator is complete)
 #pragma unroll 1
                         for (int q8 = 0; q8 < 8; ++q8) {
                             float ov[16];
@@ -692,114 +848,109 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     l *= c;
                     mref = mnew;
                 }
-                const float2 rs2 = make_float2(rs, rs), nm2 = make_float2(WSHIFT - mref, WSHIFT - mref);
-                float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pw[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float2 t0 = ptx::ffma2(make_float2(sc[32 * h + i], sc[32 * h + i + 1]), rs2, nm2);
-                        const float2 t1 = ptx::ffma2(make_float2(sc[32 * h + i + 2], sc[32 * h + i + 3]), rs2, nm2);
-                        const float2 p0 = make_float2(ptx::ex2(t0.x), ptx::ex2(t0.y));
-                        const float2 p1 = make_float2(ptx::ex2(t1.x), ptx::ex2(t1.y));
-                        acc0 = ptx::fadd2(acc0, p0);
-                        acc1 = ptx::fadd2(acc1, p1);
-                        pw[i / 2] = ptx::pack_half2(p0.x, p0.y);
-                        pw[i / 2 + 1] = ptx::pack_half2(p1.x, p1.y);
-                    }
-                    tc::st_16cols_u(tmem + lanes + TM_S + BK * g + 16 * h, pw);
-                }
-                l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                l += sum;
+                tc::st_16cols_u(tmem + lanes + TM_S + BK * g, *reinterpret_cast<const uint32_t (*)[16]>(&pw[0]));
+                tc::st_16cols_u(tmem + lanes + TM_S + BK * g + 16, *reinterpret_cast<const uint32_t (*)[16]>(&pw[16]));
                 tc::st_wait();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(B_PFULL + g));
             }
-            // ---- the segment's end: the stream's last P V, then both streams
-            // are joined (each warp takes half of the channels)
+            // ---- the segment's end: the stream's last P V; two streams over
+            // the same rows are joined
             {
-                const int last = gend - 1 - ((gend - 1 - g) & 1);  // the stream's last tile, if it had one
-                if (!dead && last >= gfirst) dead = !wait(B_PV + g, (last >> 1) & 1);
+                const int last = pair ? gend - 1 : gend - 1 - ((gend - 1 - g) & 1);  // the stream's last tile, if any
+                if (!dead && last >= gfirst) dead = !wait(B_PV + g, (pair ? last : last >> 1) & 1);
                 gi = gend;
                 ml[g * BM + r] = mref;
                 ml[(2 + g) * BM + r] = l;
             }
-            if (ptx::named_barrier_or(2, 2 * aw * 32, dead)) goto softmax_done;
+            // (after a wait that ran out every softmax warp leaves here)
+            if (ptx::named_barrier_or(2, soft_threads, dead)) goto softmax_done;
             tc::fence_after_sync();
             {
-                const float mo = ml[(1 - g) * BM + r], lo = ml[(3 - g) * BM + r];
-                const float M = fmaxf(mref, mo);
-                const float wm = ptx::ex2(mref - M), wo = ptx::ex2(mo - M);
-                const float L = l * wm + lo * wo;
-                const float w0 = g ? wo : wm, w1 = g ? wm : wo;  // weights of streams 0 and 1
-                const bool two = s.j1 - s.j0 > 1;                // (with one tile the other accumulator holds nothing)
-                const int only = gfirst & 1;                     // the stream of the first tile
+                float M = mref, L = l, w0 = 1.f, w1 = 0.f;
+                uint32_t o0 = tmem + lanes + TM_O + D * g, o1 = o0;  // this row's accumulators and their weights
+                const bool two = !pair && s.j1 - s.j0 > 1;           // (with one tile the other stream has nothing)
+                if (!pair) {
+                    const float mo = ml[(1 - g) * BM + r], lo = ml[(3 - g) * BM + r];
+                    M = fmaxf(mref, mo);
+                    w0 = ptx::ex2(mref - M);
+                    w1 = ptx::ex2(mo - M);
+                    L = l * w0 + lo * w1;
+                    o1 = tmem + lanes + TM_O + D * (1 - g);
+                    if (!two && (gfirst & 1) != g) {
+                        o0 = o1;
+                        w0 = w1;
+                    }
+                }
                 // 8 joined channels from column c
                 auto joined = [&](int c, float (&v)[8]) {
                     float u[8];
-                    ld_8cols(tmem + lanes + TM_O + D * only + c, v);
-                    if (two) ld_8cols(tmem + lanes + TM_O + D * (1 - only) + c, u);
+                    ld_8cols(o0 + c, v);
+                    if (two) ld_8cols(o1 + c, u);
                     tc::ld_wait();
-                    const float wv = only ? w1 : w0, wu = only ? w0 : w1;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = two ? v[i] * wv + u[i] * wu : v[i] * wv;
+                    for (int i = 0; i < 8; ++i) v[i] = two ? v[i] * w0 + u[i] * w1 : v[i] * w0;
                 };
                 const volatile uint32_t* seg = reinterpret_cast<const volatile uint32_t*>(smem + SM_SEG);
                 const bool cut = a.spread && (P[s.u] < seg[0] || P[s.u + 1] > seg[1]);
                 if (cut) {
                     const int cb = static_cast<int>(blockIdx.x), ca = block_of(P[s.u], P[U], seg[3]);
-                    float* mine = a.parts + static_cast<size_t>(part_slot(cb, ca)) * PART_FLOATS;
+                    float* mine = a.parts + static_cast<size_t>(part_slot(cb, ca)) * part_floats(a.part_rows);
 #pragma unroll 1
-                    for (int c = 64 * g; c < 64 * g + 64; c += 8) {
+                    for (int c = 64 * h0; c < 64 * h1; c += 8) {
                         float v[8];
                         joined(c, v);
                         if (row_ok) {
-#pragma unroll
-                            for (int i = 0; i < 8; i += 4)
-                                *reinterpret_cast<float4*>(mine + r * D + c + i) =
-                                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                            float4* p = reinterpret_cast<float4*>(mine + static_cast<size_t>(ur) * D + c);
+                            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+                            p[1] = make_float4(v[4], v[5], v[6], v[7]);
                         }
                         __syncwarp();
                     }
-                    if (g == 0 && row_ok) {
-                        mine[BM * D + r] = piece_reference(M, L);
-                        mine[BM * D + BM + r] = L;
+                    if (row_ok && (pair || g == 0)) {
+                        mine[a.part_rows * D + ur] = piece_reference(M, L);
+                        mine[a.part_rows * (D + 1) + ur] = L;
                     }
                 } else {
-                    float o[64];
                     const float inv = (L == 0.f ? 0.f : a.out_scale / L) * (VB < 8 ? rsqrt_d : 1.f);
-                    if constexpr (VB < 8) {
+#pragma unroll 1
+                    for (int h = h0; h < h1; ++h) {
+                        float o[64];
+                        if constexpr (VB < 8) {
 #pragma unroll
-                        for (int c = 0; c < 64; c += 8) {
-                            float v[8], u[8];
-                            joined(c, v);
-                            joined(64 + c, u);
+                            for (int c = 0; c < 64; c += 8) {
+                                float v[8], u[8];
+                                joined(c, v);
+                                joined(64 + c, u);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) o[c + i] = g ? v[i] - u[i] : v[i] + u[i];
-                        }
-                        fwht64(o);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 64; c += 8) {
-                            float v[8];
-                            joined(64 * g + c, v);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) o[c + i] = v[i];
-                        }
-                    }
-                    if (row_ok) {
-#pragma unroll
-                        for (int c = 0; c < 64; c += 8) {
-                            float y[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int i = c + e;
-                                y[e] = o[i] * inv;
-                                if constexpr (VB < 8) y[e] = flip_sign(y[e], (a.signs[2 * g + (i >> 5)] >> (i & 31)) & 1u);
+                                for (int i = 0; i < 8; ++i) o[c + i] = h ? v[i] - u[i] : v[i] + u[i];
                             }
-                            store_row<8>(a.out, qoff + 64 * g + c, y, a.out_dtype);
+                            fwht64(o);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 64; c += 8) {
+                                float v[8];
+                                joined(64 * h + c, v);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) o[c + i] = v[i];
+                            }
                         }
+                        if (row_ok) {
+#pragma unroll
+                            for (int c = 0; c < 64; c += 8) {
+                                float y[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const int i = c + e;
+                                    y[e] = o[i] * inv;
+                                    if constexpr (VB < 8) y[e] = flip_sign(y[e], (a.signs[2 * h + (i >> 5)] >> (i & 31)) & 1u);
+                                }
+                                store_row<8>(a.out, qoff + 64 * h + c, y, a.out_dtype);
+                            }
+                        }
+                        __syncwarp();
                     }
                 }
             }

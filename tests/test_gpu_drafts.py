@@ -205,6 +205,9 @@ TREE = [  # d, hq, hkv, kb, vb, qjl, bases, drafts, page, q dtype, out dtype
     (128, 8, 2, 8, 8, 0, [300, 77], 9, 32, FP32, FP32),
     (128, 8, 2, 4, 8, 0, [150], 21, 0, BF16, FP16),
     (128, 8, 2, 3, 2, 64, [200, 90], 12, 0, BF16, FP32),
+    (128, 8, 2, 4, 2, 0, [700, 0, 63], 64, 0, BF16, BF16),
+    (128, 16, 1, 3, 4, 0, [515, 300], 50, 48, FP16, BF16),
+    (128, 10, 2, 8, 3, 0, [1300], 27, 0, FP32, BF16),
     (64, 16, 4, 8, 8, 0, [777, 1500], 17, 0, BF16, BF16),
     (64, 6, 2, 4, 2, 32, [100], 5, 16, FP32, FP32),
     (256, 8, 2, 4, 4, 0, [119, 333], 30, 64, FP16, FP16),
