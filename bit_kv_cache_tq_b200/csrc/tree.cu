@@ -316,9 +316,70 @@ __global__ void __launch_bounds__(MERGE_THREADS) tree_general_merge_kernel(const
         r, dst);
 }
 
-// The rows of the units that the tensor-memory kernel cut between blocks
-// (it wrote the others' outputs itself), one warp per row.
-__global__ void __launch_bounds__(MERGE_THREADS) tree_mma_merge_kernel(const __grid_constant__ Args a, int nblocks) {
+// The queries of the tensor-memory kernel, once a call: rotated (turbo keys),
+// times the softmax scale and the inverse key-table scale in log2 units, as
+// one or two fp16 terms in the order its threads load them.  A row on 4 lanes,
+// 32 channels each (the chunks of the encoders), 8 rows a warp.
+__global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ Args a) {
+    constexpr int D = mma::D, LPV = D / 32;
+    ptx::wait_prerequisites();
+    ptx::launch_dependents();
+    const int lane = threadIdx.x & 31, sub = lane % LPV;
+    const long long row = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 8 + lane / LPV;
+    const int u = static_cast<int>(row / a.part_rows), ur = static_cast<int>(row % a.part_rows);
+    if (u >= a.units) return;  // (whole warps: part_rows is a multiple of 32)
+    const int G = a.group, rt = ur / G, rh = ur % G;
+    const int qt = u % a.qtiles, kv = (u / a.qtiles) % a.hkv, b = u / a.qtiles / a.hkv, t = qt * a.tok_per_tile + rt;
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = 0.f;
+    if (rt < a.tok_per_tile && t < a.n_draft) {
+        const size_t off = ((static_cast<size_t>(b) * a.n_draft + t) * a.hq + kv * G + rh) * D;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const size_t at = off + 8 * (sub + LPV * k);
+            load4(a.q, at, a.q_dtype, *reinterpret_cast<float (*)[4]>(&x[8 * k]));
+            load4(a.q, at + 4, a.q_dtype, *reinterpret_cast<float (*)[4]>(&x[8 * k + 4]));
+        }
+    }
+    __syncwarp();
+    float scale = a.score_scale;
+    if (a.k_bits != 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[8 * k + e] = flip_sign(x[8 * k + e], sign_bit(a.signs, 8 * (sub + LPV * k) + e));
+        fwht_registers(x);
+        fwht_lanes<32, LPV>(x, sub);
+        scale *= 0.08838834764831845f;  // 1 / sqrt(128)
+    }
+    uint4* dst = reinterpret_cast<uint4*>(a.prep + static_cast<size_t>(u) * mma::prep_bytes(a.part_rows, a.pair)) + ur;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float v0 = x[8 * k + 2 * e] * scale, v1 = x[8 * k + 2 * e + 1] * scale;
+            if (fabsf(v0) > mma::QLIMIT) v0 = copysignf(mma::QLIMIT, v0);  // (NaN stays)
+            if (fabsf(v1) > mma::QLIMIT) v1 = copysignf(mma::QLIMIT, v1);
+            hi[e] = ptx::pack_half2(v0, v1);
+            const float2 h = mma::half2_float2(hi[e]);
+            lo[e] = ptx::pack_half2(v0 - h.x, v1 - h.y);
+        }
+        const size_t c = static_cast<size_t>(sub + LPV * k) * a.part_rows;
+        dst[c] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (!a.pair) dst[16 * static_cast<size_t>(a.part_rows) + c] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+}
+
+// The rows of the units that the tensor-memory kernel cut between blocks (it
+// wrote the others' outputs itself): block (unit, 8 rows).  A warp per row
+// finds the pieces' weights 2^(m - M) / sum; then thread (row, 4 channels)
+// adds its channels over the pieces, whose rows lie next to each other, and a
+// warp per row applies the inverse rotation.
+constexpr int MM_ROWS = 8, MM_THREADS = 256, MM_BATCH = 8;
+__global__ void __launch_bounds__(MM_THREADS) tree_mma_merge_kernel(const __grid_constant__ Args a, int nblocks) {
+    extern __shared__ float mm_smem[];  // weights [pieces][8], then rows [8][128 + 4]
     ptx::wait_prerequisites();  // launched as a programmatic dependent of the attention kernel
     ptx::launch_dependents();
     const int u = static_cast<int>(blockIdx.x);
@@ -328,26 +389,88 @@ __global__ void __launch_bounds__(MERGE_THREADS) tree_mma_merge_kernel(const __g
     const int ca = mma::block_of(pu, total, C), cz = mma::block_of(pn - 1, total, C);
     if (ca == cz) return;
     const Unit x = unit_of<mma::BK>(a, u);
-    const int r = static_cast<int>(blockIdx.y) * (MERGE_THREADS / 32) + (static_cast<int>(threadIdx.x) >> 5);
-    const int G = a.group, t = r / G, g = r % G;
+    const int G = a.group, r0 = static_cast<int>(blockIdx.y) * MM_ROWS;
+    if (r0 / G >= x.ntok) return;
+    const int np = cz - ca + 1, R = a.part_rows, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float* wts = mm_smem;
+    float* rows = mm_smem + ((np * MM_ROWS + 3) & ~3);
+    const size_t slot = mma::part_floats(R);
+    auto piece = [&](int j) { return a.parts + static_cast<size_t>(mma::part_slot(ca + j, ca)) * slot; };
+    {
+        const int r = r0 + warp;
+        const bool in = r / G < x.ntok;  // (other rows hold nothing)
+        float M = -INFINITY, L = 0.f;
+        for (int j = lane; j < np; j += 32) {
+            const float m = in ? __ldcg(piece(j) + R * mma::D + r) : -INFINITY;
+            wts[j * MM_ROWS + warp] = m;
+            M = fmaxf(M, m);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+        for (int j = lane; j < np; j += 32) {
+            const float m = wts[j * MM_ROWS + warp];
+            float w = 0.f;
+            if (m > -INFINITY) {
+                w = ptx::ex2(m - M);
+                L = fmaf(__ldcg(piece(j) + R * (mma::D + 1) + r), w, L);
+            }
+            wts[j * MM_ROWS + warp] = w;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(kFullMask, L, o);
+        const float inv = L == 0.f ? 0.f : a.out_scale / L;  // (NaN stays NaN)
+        for (int j = lane; j < np; j += 32) wts[j * MM_ROWS + warp] *= inv;
+    }
+    __syncthreads();
+    {
+        const int r = tid & 7, chunk = tid >> 3;
+        const size_t at = (static_cast<size_t>(chunk) * R + r0 + r) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = 0; j0 < np; j0 += MM_BATCH) {
+            float4 v[MM_BATCH];
+            float w[MM_BATCH];
+#pragma unroll
+            for (int k = 0; k < MM_BATCH; ++k) {
+                w[k] = j0 + k < np ? wts[(j0 + k) * MM_ROWS + r] : 0.f;
+                // (rows that were never written, or weigh nothing, are not read)
+                v[k] = w[k] != 0.f ? __ldcg(reinterpret_cast<const float4*>(piece(j0 + k) + at))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < MM_BATCH; ++k) {
+                acc.x = fmaf(v[k].x, w[k], acc.x);
+                acc.y = fmaf(v[k].y, w[k], acc.y);
+                acc.z = fmaf(v[k].z, w[k], acc.z);
+                acc.w = fmaf(v[k].w, w[k], acc.w);
+            }
+        }
+        *reinterpret_cast<float4*>(rows + r * (mma::D + 4) + 4 * chunk) = acc;
+    }
+    __syncthreads();
+    const int r = r0 + warp, t = r / G, g = r % G;
     if (t >= x.ntok) return;
-    const size_t dst = ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + t) * a.hq + x.kv * G + g) * mma::D;
-    const size_t slot = mma::part_floats(a.part_rows);
-    merge_row<mma::D>(
-        a, [&](int j) { return a.parts + static_cast<size_t>(mma::part_slot(ca + j, ca)) * slot; }, cz - ca + 1,
-        a.part_rows, r, dst);
+    const float4 y = *reinterpret_cast<const float4*>(rows + warp * (mma::D + 4) + 4 * lane);
+    float e[4] = {y.x, y.y, y.z, y.w};
+    if (a.v_bits != 8) {
+        fwht_registers(e);
+        fwht_lanes<4, 32>(e, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = flip_sign(e[i] * 0.08838834764831845f, sign_bit(a.signs, 4 * lane + i));
+    }
+    store_row<4>(a.out, ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + t) * a.hq + x.kv * G + g) * mma::D + 4 * lane, e,
+                 a.out_dtype);
 }
 
 // Work layout of a call.  general: n_split blocks per unit of GEN_ROWS rows.
 // Tensor-memory kernel: units of up to 128 rows, or (pair) 256 where a kv head
 // has more than 128 (its drafts spread evenly over its units), the
 // tile sequence shared by one block per SM (spread) or, past SCHED_MAX units,
-// a block per unit; workspace: the schedule, then two partial outputs per
-// block.
+// a block per unit; workspace: the prepared queries, then (spread) the schedule
+// and two partial outputs per block.
 struct Plan {
     long long units;
     int tok_per_tile, qtiles, n_split, spread, blocks, pair, part_rows;
-    size_t sched_bytes, bytes;
+    size_t prep_bytes, sched_bytes, bytes;
 };
 
 static bool mma_supported(const tq_params& p) { return p.head_dim == mma::D && p.qjl_dims == 0; }
@@ -364,9 +487,11 @@ static Plan mma_plan(const tq_params& p, int batch, int n_draft, int sms, bool m
     pl.units = static_cast<long long>(batch) * p.num_kv_heads * pl.qtiles;
     pl.spread = pl.units <= mma::SCHED_MAX;
     pl.blocks = pl.spread ? sms : static_cast<int>(pl.units);
+    pl.prep_bytes = static_cast<size_t>(pl.units) * mma::prep_bytes(pl.part_rows, pl.pair);
+    pl.bytes = pl.prep_bytes;
     if (pl.spread) {
         pl.sched_bytes = (static_cast<size_t>(pl.units + 1) * 4 + 255) / 256 * 256;
-        pl.bytes = pl.sched_bytes + 2ull * pl.blocks * mma::part_floats(pl.part_rows) * sizeof(float);
+        pl.bytes += pl.sched_bytes + 2ull * pl.blocks * mma::part_floats(pl.part_rows) * sizeof(float);
     }
     return pl;
 }
@@ -396,7 +521,9 @@ static cudaError_t launch_general(const Args& a, cudaStream_t s) {
 }
 
 static cudaError_t launch_mma(const Args& a, const Plan& pl, cudaStream_t s) {
-    cudaError_t e;
+    const long long warps = pl.units * a.part_rows / 8;
+    cudaError_t e = mma::launch_dependent(tree_prep_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0u, s, a);
+    if (e != cudaSuccess) return e;
     switch (a.k_bits) {
         case 2: e = launch_mma_k2(a.v_bits, a, pl.blocks, s); break;
         case 3: e = launch_mma_k3(a.v_bits, a, pl.blocks, s); break;
@@ -404,9 +531,10 @@ static cudaError_t launch_mma(const Args& a, const Plan& pl, cudaStream_t s) {
         default: e = launch_mma_k8(a.v_bits, a, pl.blocks, s); break;
     }
     if (e != cudaSuccess || !pl.spread) return e;
-    const int rows = (a.tok_per_tile * a.group + MERGE_THREADS / 32 - 1) / (MERGE_THREADS / 32);
+    const int rows = (a.tok_per_tile * a.group + MM_ROWS - 1) / MM_ROWS;
+    const uint32_t smem = (pl.blocks * MM_ROWS + 4 + MM_ROWS * (mma::D + 4)) * 4u;
     return mma::launch_dependent(tree_mma_merge_kernel, dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(rows)),
-                                 dim3(MERGE_THREADS), 0u, s, a, pl.blocks);
+                                 dim3(MM_THREADS), smem, s, a, pl.blocks);
 }
 
 static Plan plan_of(const tq_params& p, int batch, int n_draft, int sms, int out_dtype) {
@@ -441,13 +569,11 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
         // the shared tile sequence is counted in 32 bits: a block per unit instead
         pl.spread = 0;
         pl.blocks = static_cast<int>(pl.units);
-        pl.bytes = 0;
+        pl.bytes = pl.prep_bytes;
     }
-    if (pl.bytes > 0) {
-        if (!d_workspace) return TQ_ERR_INVALID_ARG;
-        if (workspace_bytes < pl.bytes) return TQ_ERR_CAPACITY;
-        if (!aligned16(d_workspace)) return TQ_ERR_ALIGNMENT;
-    }
+    if (!d_workspace) return TQ_ERR_INVALID_ARG;
+    if (workspace_bytes < pl.bytes) return TQ_ERR_CAPACITY;
+    if (!aligned16(d_workspace)) return TQ_ERR_ALIGNMENT;
     if (mm) {  // (the code tables' lookups carry their shared-window addresses)
         int reserved = 0, dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -469,8 +595,9 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     a.draft_lens = d_draft_lens;
     a.out = d_out;
     a.err = d_error;
-    a.sched = static_cast<uint32_t*>(d_workspace);
-    a.parts = reinterpret_cast<float*>(static_cast<char*>(d_workspace) + pl.sched_bytes);
+    a.prep = static_cast<uint8_t*>(d_workspace);
+    a.sched = reinterpret_cast<uint32_t*>(a.prep + pl.prep_bytes);
+    a.parts = reinterpret_cast<float*>(a.prep + pl.prep_bytes + pl.sched_bytes);
     a.capacity = capacity;
     if (pm) {
         a.table = pm->table;

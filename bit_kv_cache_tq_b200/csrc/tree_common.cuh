@@ -37,6 +37,7 @@ struct Args {
     uint32_t* err;
     float* parts;                // partial results (see the kernels)
     uint32_t* sched;             // [units + 1] (tensor-memory kernel)
+    uint8_t* prep;               // prepared queries (tensor-memory kernel)
     const int32_t* table;        // paged, or null
     int max_blocks, block_size, num_blocks;
     int q_dtype, out_dtype, batch, hq, hkv, group, capacity, n_draft;

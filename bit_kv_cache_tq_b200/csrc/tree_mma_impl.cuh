@@ -16,6 +16,9 @@
 // so only bf16 outputs, whose rounding (2^-8) hides that of one-term queries
 // (2^-11 of each coordinate), are paired.
 //
+// The queries come from a small kernel before this one (tree_prep_kernel):
+// rotated once, scaled, as fp16 terms in the order a block's threads load them.
+//
 // Roles (20 warps):
 //  * producer (1 warp): bulk copies of packed codes and norms into a ring (and
 //    2 warps that load the norms where a cache's rows of norms are not 16-byte
@@ -26,9 +29,9 @@
 //  * MMA issuer (1 warp): S = (Qhi + Qlo) K~^T (M = 128, N = 64, K = 128) and O += P V~
 //    (M = 128, N = 128, K = 64), the queries and the weights as A operands in
 //    tensor memory;
-//  * softmax (2 x 4 warps, one query row a thread): the queries enter scaled
-//    by the softmax scale (log2 units), so a weight is 2^(S n - reference),
-//    n the key's norm.  There is no pass for the maximum: a row's reference is raised only when
+//  * softmax (2 x 4 warps, one query row a thread): the queries are scaled by
+//    the softmax scale (log2 units), so a weight is 2^(S n - reference), n the
+//    key's norm.  There is no pass for the maximum: a row's reference is raised only when
 //    the tile's sum of weights shows that one of them may pass the fp16 range
 //    (always on a stream's first tile), and the tile is then done again.
 //    Weights overwrite the scores.
@@ -76,6 +79,10 @@ constexpr long long WAIT_LIMIT = 2000000000ll;  // clock cycles (~1 s)
 // tile's sum passes WLIMIT, below which no single weight leaves the fp16 range.
 constexpr float WSHIFT = 6.0f, WLIMIT = 32768.0f;
 constexpr float QLIMIT = 60000.0f;  // scaled queries past the fp16 range are cut (their scores pass 10^4 either way)
+
+// Prepared queries of a unit: per fp16 term, 16 chunks of 8 channels of every
+// row, the rows of a chunk next to each other.
+__host__ __device__ constexpr size_t prep_bytes(int rows, bool pair) { return static_cast<size_t>(rows) * D * (pair ? 2 : 4); }
 
 __host__ __device__ constexpr int row_bytes(int bits) { return bits == 8 ? D : D * bits / 8; }
 // Shared memory (offsets from a 1024-byte aligned base).
@@ -170,7 +177,8 @@ __device__ __forceinline__ int block_of(uint32_t g, uint32_t total, uint32_t nbl
 }
 // A block holds at most two pieces of cut units: the head of the unit its
 // range starts (slot 2c + 1) and a piece of a unit begun earlier (slot 2c).
-// A slot is [rows][D] fp32, then m and l.
+// A slot is 32 chunks of 4 channels of every row, fp32, the rows of a chunk
+// next to each other; then the rows' m and l.
 __host__ __device__ constexpr size_t part_floats(int rows) { return static_cast<size_t>(rows) * (D + 2); }
 __device__ __forceinline__ int part_slot(int block, int first_block) { return 2 * block + (block == first_block); }
 
@@ -284,58 +292,7 @@ __device__ __forceinline__ float2 half2_float2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// Walsh-Hadamard butterflies over 64 values.
-__device__ __forceinline__ void fwht64(float (&x)[64]) { fwht_registers(x); }
 
-// This half's 64 values of a query row after the first butterfly stage
-// (x[i] +- x[i + 64], signs applied), or (int8 keys) the half itself.  Four
-// 16-byte loads are in flight at a time.
-template <int DTYPE, bool ROTATE>
-__device__ __forceinline__ void load_half_typed(const Args& a, size_t off, int half, float (&x)[64]) {
-    constexpr int E = DTYPE == 0 ? 4 : 8;  // elements of a 16-byte load
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + off * (DTYPE == 0 ? 4 : 2));
-    auto value = [](const uint4& w, int e) -> float {
-        const uint32_t u = DTYPE == 0 ? (e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w)
-                                      : (e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w);
-        if (DTYPE == 0) return __uint_as_float(u);
-        if (DTYPE == 1) return __uint_as_float((e & 1) ? u & 0xffff0000u : u << 16);
-        const __half2 h = *reinterpret_cast<const __half2*>(&u);
-        return (e & 1) ? __high2float(h) : __low2float(h);
-    };
-#pragma unroll
-    for (int c = 0; c < 64; c += 2 * E) {
-        uint4 lo[2], hi[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (ROTATE) {
-                lo[i] = p[c / E + i];
-                hi[i] = p[64 / E + c / E + i];
-            } else {
-                lo[i] = p[(64 / E) * half + c / E + i];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int k = c + E * i + e;
-                if (ROTATE) {
-                    const float u = flip_sign(value(lo[i], e), (a.signs[k >> 5] >> (k & 31)) & 1u);
-                    const float v = flip_sign(value(hi[i], e), (a.signs[2 + (k >> 5)] >> (k & 31)) & 1u);
-                    x[k] = half ? u - v : u + v;
-                } else {
-                    x[k] = value(lo[i], e);
-                }
-            }
-        asm volatile("" ::: "memory");
-    }
-}
-template <bool ROTATE>
-__device__ __forceinline__ void load_half(const Args& a, size_t off, int half, float (&x)[64]) {
-    if (a.q_dtype == TQ_BF16) load_half_typed<1, ROTATE>(a, off, half, x);
-    else if (a.q_dtype == TQ_F16) load_half_typed<2, ROTATE>(a, off, half, x);
-    else load_half_typed<0, ROTATE>(a, off, half, x);
-}
 
 // 8 consecutive fp32 columns of this thread's tensor-memory lane.
 __device__ __forceinline__ void ld_8cols(uint32_t taddr, float (&v)[8]) {
@@ -725,33 +682,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 }
                 continue;
             }
-            // ---- the row's queries, in log2 units of the score per unit of the key
-#pragma unroll 1
-            for (int h = h0; h < h1; ++h) {
-                float q[64];
-                if (row_ok) {
-                    load_half<(KB < 8)>(a, qoff, h, q);
-                } else {
+            // ---- queries: the row block's (pair), or the first stream's
+            // warps move the first term and the second's the second
+            {
+                const uint4* src = reinterpret_cast<const uint4*>(a.prep + static_cast<size_t>(s.u) * prep_bytes(a.part_rows, pair)) +
+                                   (pair ? 0 : static_cast<size_t>(g) * 16 * a.part_rows) + ur;
+                uint4 w[16];
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) q[i] = 0.f;
-                }
-                __syncwarp();
-                if constexpr (KB < 8) fwht64(q);
-                const float scale = KB < 8 ? a.score_scale * rsqrt_d : a.score_scale;
+                for (int c = 0; c < 16; ++c) w[c] = src[static_cast<size_t>(c) * a.part_rows];
 #pragma unroll
-                for (int c = 0; c < 64; c += 16) {
-                    uint32_t hw[8], lw[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float v0 = q[c + 2 * e] * scale, v1 = q[c + 2 * e + 1] * scale;
-                        if (fabsf(v0) > QLIMIT) v0 = copysignf(QLIMIT, v0);  // (NaN stays)
-                        if (fabsf(v1) > QLIMIT) v1 = copysignf(QLIMIT, v1);
-                        hw[e] = ptx::pack_half2(v0, v1);
-                        const float2 hf = half2_float2(hw[e]);
-                        lw[e] = ptx::pack_half2(v0 - hf.x, v1 - hf.y);
-                    }
-                    tc::st_8cols(tmem + lanes + TM_Q + (pair ? 64 * g : 0) + 32 * h + c / 2, hw);
-                    if (!pair) tc::st_8cols(tmem + lanes + TM_Q + 64 + 32 * h + c / 2, lw);
+                for (int c = 0; c < 16; c += 4) {
+                    const uint32_t v[16] = {w[c].x,     w[c].y,     w[c].z,     w[c].w,     w[c + 1].x, w[c + 1].y,
+                                            w[c + 1].z, w[c + 1].w, w[c + 2].x, w[c + 2].y, w[c + 2].z, w[c + 2].w,
+                                            w[c + 3].x, w[c + 3].y, w[c + 3].z, w[c + 3].w};
+                    tc::st_16cols_u(tmem + lanes + TM_Q + 64 * g + 4 * c, v);
                 }
             }
             tc::st_wait();
@@ -903,9 +847,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                         float v[8];
                         joined(c, v);
                         if (row_ok) {
-                            float4* p = reinterpret_cast<float4*>(mine + static_cast<size_t>(ur) * D + c);
+                            float4* p = reinterpret_cast<float4*>(mine) + static_cast<size_t>(c / 4) * a.part_rows + ur;
                             p[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+                            p[a.part_rows] = make_float4(v[4], v[5], v[6], v[7]);
                         }
                         __syncwarp();
                     }
@@ -927,7 +871,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) o[c + i] = h ? v[i] - u[i] : v[i] + u[i];
                             }
-                            fwht64(o);
+                            fwht_registers(o);
                         } else {
 #pragma unroll
                             for (int c = 0; c < 64; c += 8) {
