@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
         fwht_lanes<32, LPV>(x, sub);
         scale *= 0.08838834764831845f;  // 1 / sqrt(128)
     }
-    uint4* dst = reinterpret_cast<uint4*>(a.prep + static_cast<size_t>(u) * mma::prep_bytes(a.part_rows, a.pair)) + ur;
+    uint4* dst = reinterpret_cast<uint4*>(a.prep + static_cast<size_t>(u) * mma::prep_bytes(a.part_rows, a.terms)) + ur;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         uint32_t hi[4], lo[4];
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
         }
         const size_t c = static_cast<size_t>(sub + LPV * k) * a.part_rows;
         dst[c] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (!a.pair) dst[16 * static_cast<size_t>(a.part_rows) + c] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (a.terms == 2) dst[16 * static_cast<size_t>(a.part_rows) + c] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
@@ -469,16 +469,17 @@ __global__ void __launch_bounds__(MM_THREADS) tree_mma_merge_kernel(const __grid
 // and two partial outputs per block.
 struct Plan {
     long long units;
-    int tok_per_tile, qtiles, n_split, spread, blocks, pair, part_rows;
+    int tok_per_tile, qtiles, n_split, spread, blocks, pair, terms, part_rows;
     size_t prep_bytes, sched_bytes, bytes;
 };
 
 static bool mma_supported(const tq_params& p) { return p.head_dim == mma::D && p.qjl_dims == 0; }
 
-static Plan mma_plan(const tq_params& p, int batch, int n_draft, int sms, bool may_pair) {
+static Plan mma_plan(const tq_params& p, int batch, int n_draft, int sms, bool one_term) {
     Plan pl{};
     const int group = p.num_q_heads / p.num_kv_heads;
-    pl.pair = may_pair && n_draft > mma::BM / group;
+    pl.terms = one_term ? 1 : 2;
+    pl.pair = one_term && n_draft > mma::BM / group;
     const int most = (pl.pair ? 2 * mma::BM : mma::BM) / group;
     pl.qtiles = (n_draft + most - 1) / most;
     pl.tok_per_tile = (n_draft + pl.qtiles - 1) / pl.qtiles;
@@ -487,7 +488,7 @@ static Plan mma_plan(const tq_params& p, int batch, int n_draft, int sms, bool m
     pl.units = static_cast<long long>(batch) * p.num_kv_heads * pl.qtiles;
     pl.spread = pl.units <= mma::SCHED_MAX;
     pl.blocks = pl.spread ? sms : static_cast<int>(pl.units);
-    pl.prep_bytes = static_cast<size_t>(pl.units) * mma::prep_bytes(pl.part_rows, pl.pair);
+    pl.prep_bytes = static_cast<size_t>(pl.units) * mma::prep_bytes(pl.part_rows, pl.terms);
     pl.bytes = pl.prep_bytes;
     if (pl.spread) {
         pl.sched_bytes = (static_cast<size_t>(pl.units + 1) * 4 + 255) / 256 * 256;
@@ -621,6 +622,7 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     a.n_split = pl.n_split;
     a.spread = pl.spread;
     a.pair = pl.pair;
+    a.terms = pl.terms;
     a.part_rows = pl.part_rows;
     a.staged_norms = pm || capacity % 8 == 0;
     const double rd = std::sqrt(static_cast<double>(p.head_dim));

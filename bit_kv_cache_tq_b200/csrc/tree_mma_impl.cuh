@@ -11,10 +11,14 @@
 // the tiles alternate between the streams, which are joined at the end of a
 // unit's run (a row's two accumulators lie in one tensor-memory lane).  Units
 // of up to 256 rows (`pair`): each stream has half of the rows and both read
-// every tile, so a dequantised tile serves twice the rows.  The second row
-// block's queries take the tensor memory of the queries' second fp16 term,
-// so only bf16 outputs, whose rounding (2^-8) hides that of one-term queries
-// (2^-11 of each coordinate), are paired.
+// every tile, so a dequantised tile serves twice the rows.
+//
+// Queries enter as fp16 terms (a.terms): two for fp16 and fp32 outputs, so
+// that a score keeps about 22 bits of its query; one for bf16 outputs, whose
+// rounding (2^-8) hides that of the queries (2^-11 of each coordinate).  The
+// second term's tensor memory then holds the second row block's queries (pair)
+// or the weights, which otherwise overwrite the scores (overlay) and hold the
+// stream's next scores back until they are used.
 //
 // The queries come from a small kernel before this one (tree_prep_kernel):
 // rotated once, scaled, as fp16 terms in the order a block's threads load them.
@@ -34,7 +38,6 @@
 //    key's norm.  There is no pass for the maximum: a row's reference is raised only when
 //    the tile's sum of weights shows that one of them may pass the fp16 range
 //    (always on a stream's first tile), and the tile is then done again.
-//    Weights overwrite the scores.
 //
 // What bounds it is the shared-memory and tensor-memory data path: a tile of
 // 64 keys moves, in 128-byte passes, 256 for the scores, 128 for the weights
@@ -69,8 +72,9 @@ static_assert(SOFTMAX_WARPS * 32 * REGS_SOFTMAX + DEQ_WARPS * 32 * REGS_DEQ + 12
                   NTHREADS * REGS_LAUNCH,
               "the register split draws on what the block was launched with");
 // tensor-memory columns (32-bit; fp16 operands take two elements a column)
-constexpr uint32_t TM_Q = 0;     // scaled queries, fp16 [128][128], and their remainder or (pair) the second row block's
-constexpr uint32_t TM_S = 128;   // 2 x fp32 scores [128][64]; the weights, fp16, over their first half
+constexpr uint32_t TM_Q = 0;     // scaled queries, fp16 [128][128]; then their second term, or (pair) the second row
+                                 // block's, or the weights, 2 x fp16 [128][64]
+constexpr uint32_t TM_S = 128;   // 2 x fp32 scores [128][64]; (overlay) the weights over their first half
 constexpr uint32_t TM_O = 256;   // 2 x fp32 accumulators [128][128]
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long WAIT_LIMIT = 2000000000ll;  // clock cycles (~1 s)
@@ -82,7 +86,7 @@ constexpr float QLIMIT = 60000.0f;  // scaled queries past the fp16 range are cu
 
 // Prepared queries of a unit: per fp16 term, 16 chunks of 8 channels of every
 // row, the rows of a chunk next to each other.
-__host__ __device__ constexpr size_t prep_bytes(int rows, bool pair) { return static_cast<size_t>(rows) * D * (pair ? 2 : 4); }
+__host__ __device__ constexpr size_t prep_bytes(int rows, int terms) { return static_cast<size_t>(rows) * D * 2 * terms; }
 
 __host__ __device__ constexpr int row_bytes(int bits) { return bits == 8 ? D : D * bits / 8; }
 // Shared memory (offsets from a 1024-byte aligned base).
@@ -103,7 +107,7 @@ constexpr uint32_t SM_ML = SM_KNR + 4 * BK * 2;             // float [2][2][128]
 constexpr uint32_t SM_CENT = SM_ML + 4 * BM * 4;            // fp16 centroids, keys then values
 constexpr uint32_t SM_BAR = SM_CENT + 64;
 constexpr int B_FULL = 0, B_EMPTY = NS, B_KFULL = 2 * NS, B_KEMPTY = B_KFULL + 2, B_VFULL = B_KEMPTY + 2,
-              B_VEMPTY = B_VFULL + 2, B_PV = B_VEMPTY + 2, B_SFULL = B_PV + 2, B_PFULL = B_SFULL + 2, B_QREADY = B_PFULL + 2,
+              B_VEMPTY = B_VFULL + 2, B_PV = B_VEMPTY + 2, B_SFULL = B_PV + 2, B_SEMPTY = B_SFULL + 2, B_PFULL = B_SEMPTY + 2, B_QREADY = B_PFULL + 2,
               B_FINAL = B_QREADY + 1, NBARS = B_FINAL + 1;
 constexpr uint32_t SM_TMEM = SM_BAR + NBARS * 8;
 constexpr uint32_t SM_FLAG = SM_TMEM + 4;
@@ -319,15 +323,19 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
         *abort_flag = 1;
     };
     auto wait = [&](int i, uint32_t parity) -> bool {
-        if (*abort_flag) return false;
-        if (!ptx::mbar_wait_bounded_lean(bar(i), parity, WAIT_LIMIT)) {
-            fail();
-            return false;
+        const uint32_t b = bar(i);
+        if (ptx::mbar_try_wait(b, parity)) return true;
+        const long long start = clock64();
+        while (!*abort_flag) {
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k)
+                if (ptx::mbar_try_wait(b, parity)) return true;
+            if (clock64() - start > WAIT_LIMIT) fail();
         }
-        return true;
+        return false;
     };
     const int G = a.group;
-    const bool pair = a.pair;
+    const bool pair = a.pair, two_terms = a.terms == 2, overlay = pair || two_terms;
     // softmax warps that own query rows, of each stream
     const int rows = a.tok_per_tile * G;
     const int aw0 = (min(BM, rows) + 31) / 32, aw1 = pair ? (rows - BM + 31) / 32 : aw0;
@@ -345,6 +353,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
             ptx::mbar_init(bar(B_VEMPTY + i), 1);
             ptx::mbar_init(bar(B_PV + i), 1);
             ptx::mbar_init(bar(B_SFULL + i), 1);
+            ptx::mbar_init(bar(B_SEMPTY + i), i ? aw1 : aw0);
             ptx::mbar_init(bar(B_PFULL + i), i ? aw1 : aw0);
         }
         ptx::mbar_init(bar(B_QREADY), aw0 + aw1);
@@ -540,7 +549,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     for (int ks = 0; ks < D / 16; ++ks) {
                         const uint64_t bd = kd + static_cast<uint64_t>(((ks >> 2) * (BK * 128) + (ks & 3) * 32) >> 4);
                         tc::mma_f16_ts(sd, qd + 8 * ks, bd, idesc_s, ks > 0);
-                        if (!pair) tc::mma_f16_ts(sd, qd + 64 + 8 * ks, bd, idesc_s, true);
+                        if (two_terms) tc::mma_f16_ts(sd, qd + 64 + 8 * ks, bd, idesc_s, true);
                     }
                     tc::commit(bar(B_SFULL + g));
                     if (last) tc::commit(bar(B_KEMPTY + bf));
@@ -556,9 +565,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 tc::fence_after_sync();
                 if (leader) {
                     const uint64_t vd = vdesc0 + static_cast<uint64_t>(bf * (BK * D * 2) >> 4);
+                    const uint32_t pd = tmem + (overlay ? TM_S + BK * g : TM_Q + 64 + (BK / 2) * g);
 #pragma unroll
                     for (int ks = 0; ks < BK / 16; ++ks)
-                        tc::mma_f16_ts(tmem + TM_O + D * g, tmem + TM_S + BK * g + 8 * ks,
+                        tc::mma_f16_ts(tmem + TM_O + D * g, pd + 8 * ks,
                                        vd + static_cast<uint64_t>(ks * 2048 >> 4), idesc_o, !first || ks > 0);
                     tc::commit(bar(B_PV + g));
                     if (last) tc::commit(bar(B_VEMPTY + bf));
@@ -574,8 +584,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 if (!wait(B_QREADY, qs & 1)) break;
                 ++qs;
                 const int gfirst = gi, gend = gi + (s.j1 - s.j0);
-                // (a stream's weights lie in its score buffer: its P V is
-                // waited for before the buffer is written again)
+                // (overlay: a stream's weights lie in its score buffer, so its
+                // P V is waited for before the buffer is written again)
                 if (pair) {
                     if (!issue_s(gi, 0, false) || !issue_s(gi, 1, true)) break;
                     for (; gi < gend; ++gi) {
@@ -593,8 +603,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     if (gi + 1 < gend && !issue_s(gi + 1, (gi + 1) & 1, true)) break;
                     for (; gi < gend; ++gi) {
                         const int g = gi & 1, q = gi >> 1;
+                        if (!overlay && gi + 2 < gend) {
+                            if (!wait(B_SEMPTY + g, q & 1)) goto issued;
+                            if (!issue_s(gi + 2, g, true)) goto issued;
+                        }
                         if (!issue_pv(gi, g, q, gi < gfirst + 2, true)) goto issued;
-                        if (gi + 2 < gend) {
+                        if (overlay && gi + 2 < gend) {
                             if (!wait(B_PV + g, q & 1)) goto issued;
                             if (!issue_s(gi + 2, g, true)) goto issued;
                         }
@@ -682,20 +696,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 }
                 continue;
             }
-            // ---- queries: the row block's (pair), or the first stream's
-            // warps move the first term and the second's the second
+            // ---- queries: the warps of a stream move its row block's (pair),
+            // one of two terms, or every second group of four chunks
             {
-                const uint4* src = reinterpret_cast<const uint4*>(a.prep + static_cast<size_t>(s.u) * prep_bytes(a.part_rows, pair)) +
-                                   (pair ? 0 : static_cast<size_t>(g) * 16 * a.part_rows) + ur;
-                uint4 w[16];
+                const uint4* src = reinterpret_cast<const uint4*>(a.prep + static_cast<size_t>(s.u) * prep_bytes(a.part_rows, a.terms)) +
+                                   (two_terms ? static_cast<size_t>(g) * 16 * a.part_rows : 0) + ur;
+                const uint32_t dst = tmem + lanes + TM_Q + (overlay ? 64 * g : 0);
+                const int step = overlay ? 4 : 8;
+#pragma unroll 2
+                for (int c = overlay ? 0 : 4 * g; c < 16; c += step) {
+                    uint4 w[4];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) w[c] = src[static_cast<size_t>(c) * a.part_rows];
-#pragma unroll
-                for (int c = 0; c < 16; c += 4) {
-                    const uint32_t v[16] = {w[c].x,     w[c].y,     w[c].z,     w[c].w,     w[c + 1].x, w[c + 1].y,
-                                            w[c + 1].z, w[c + 1].w, w[c + 2].x, w[c + 2].y, w[c + 2].z, w[c + 2].w,
-                                            w[c + 3].x, w[c + 3].y, w[c + 3].z, w[c + 3].w};
-                    tc::st_16cols_u(tmem + lanes + TM_Q + 64 * g + 4 * c, v);
+                    for (int i = 0; i < 4; ++i) w[i] = src[static_cast<size_t>(c + i) * a.part_rows];
+                    const uint32_t v[16] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w,
+                                            w[2].x, w[2].y, w[2].z, w[2].w, w[3].x, w[3].y, w[3].z, w[3].w};
+                    tc::st_16cols_u(dst + 4 * c, v);
                 }
             }
             tc::st_wait();
@@ -778,7 +793,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                         }
                     }
                     const float mnew = fmaxf(m, mref), c = ptx::ex2(mref - mnew);
-                    if (!first) {  // (this step's scores came after the stream's last P V: the accumulator is complete)
+                    if (!first) {
+                        // the accumulator is complete (overlay: this step's scores came after the stream's last P V)
+                        if (!overlay) {
+                            dead = !wait(B_PV + g, (q - 1) & 1);
+                            if (dead) break;
+                            tc::fence_after_sync();
+                        }
 #pragma unroll 1
                         for (int q8 = 0; q8 < 8; ++q8) {
                             float ov[16];
@@ -792,9 +813,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     l *= c;
                     mref = mnew;
                 }
+                if (dead) break;
                 l += sum;
-                tc::st_16cols_u(tmem + lanes + TM_S + BK * g, *reinterpret_cast<const uint32_t (*)[16]>(&pw[0]));
-                tc::st_16cols_u(tmem + lanes + TM_S + BK * g + 16, *reinterpret_cast<const uint32_t (*)[16]>(&pw[16]));
+                uint32_t pd = tmem + lanes + TM_S + BK * g;
+                if (!overlay) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(B_SEMPTY + g));  // the scores have been read
+                    if (!first) {  // the weights' columns are free when the stream's last P V is done
+                        dead = !wait(B_PV + g, (q - 1) & 1);
+                        if (dead) break;
+                        tc::fence_after_sync();
+                    }
+                    pd = tmem + lanes + TM_Q + 64 + (BK / 2) * g;
+                }
+                tc::st_16cols_u(pd, *reinterpret_cast<const uint32_t (*)[16]>(&pw[0]));
+                tc::st_16cols_u(pd + 16, *reinterpret_cast<const uint32_t (*)[16]>(&pw[16]));
                 tc::st_wait();
                 tc::fence_before_sync();
                 __syncwarp();
