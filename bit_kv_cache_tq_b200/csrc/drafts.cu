@@ -18,6 +18,8 @@ constexpr int MAX_PATH = 64;
 constexpr int LAYERS_PER_LAUNCH = 64;
 constexpr int THREADS = 256;
 
+constexpr int HEADS = 4;  // kv heads of one block
+
 struct Layer {
     uint8_t* k_codes;
     uint8_t* v_codes;
@@ -25,17 +27,15 @@ struct Layer {
     uint16_t* v_norms;
     uint32_t* k_qjl;
     uint16_t* k_gamma;
-    int32_t k_units, v_units, qjl_words;  // 16-byte units of a code row; 32-bit words of a sketch row
+    int32_t k_bytes, v_bytes, qjl_words;  // of one row
     int32_t hkv;
-    int32_t row0;      // index of the layer's first (sequence, kv head) block
-    int32_t capacity;  // slots of a sequence, or of a block of the pool
-    int32_t num_blocks;
 };
 
 struct Args {
     Layer layers[LAYERS_PER_LAUNCH];
-    int n_layers, batch, max_path, advance;
-    int max_blocks;            // paged: entries per sequence (0: contiguous)
+    int batch, max_path, advance, groups;  // groups: blocks per sequence (of HEADS heads), for the layer with most
+    int capacity;              // slots of a sequence, or of a block of the pool
+    int num_blocks, max_blocks;  // paged: blocks of a pool, entries per sequence
     const int32_t* table;
     const int32_t* path;       // [batch][max_path]
     const int32_t* path_lens;  // [batch]
@@ -44,64 +44,96 @@ struct Args {
     uint32_t* err;
 };
 
-// Up to N units of one array per thread, read before the barrier, written after it.
+// The rows of one array that a block moves, as units of T: thread t takes unit
+// t % lanes of every THREADS / lanes-th row, lanes being the units of a row
+// rounded up to a power of two (no division).  All of a head's rows are read
+// before any is written.
 template <typename T, int N>
-struct Held {
-    T v[N];
-};
-
-template <typename T, int N>
-__device__ __forceinline__ void load_rows(Held<T, N>& h, const T* base, const long long* from, int units, int total) {
+struct Mover {
+    T v[HEADS][N];
+    int unit, row0, shift, units;
+    __device__ __forceinline__ Mover(int row_bytes) {
+        units = row_bytes / static_cast<int>(sizeof(T));
+        shift = units <= 1 ? 0 : 32 - __clz(units - 1);
+        unit = threadIdx.x & ((1 << shift) - 1);
+        row0 = threadIdx.x >> shift;
+    }
+    // f(i, head, row, unit) over this thread's units
+    template <typename F>
+    __device__ __forceinline__ void each(int n, int heads, F f) {
+        const int step = THREADS >> shift;
+        if (unit >= units) return;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int u = threadIdx.x + i * THREADS;
-        if (u < total) {
-            const long long row = from[u / units];
-            if (row >= 0) h.v[i] = base[row * units + u % units];
+        for (int i = 0; i < N; ++i) {
+            const int r = row0 + i * step;
+            if (r < n) {
+#pragma unroll
+                for (int h = 0; h < HEADS; ++h)
+                    if (h < heads) f(i, h, r);
+            }
         }
     }
-}
-
-template <typename T, int N>
-__device__ __forceinline__ void store_rows(const Held<T, N>& h, T* base, const long long* from, const long long* to,
-                                           int units, int total) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int u = threadIdx.x + i * THREADS;
-        if (u < total && from[u / units] >= 0) base[to[u / units] * units + u % units] = h.v[i];
+    __device__ __forceinline__ void load(const void* base, const long long* from, int n, int heads, long long head) {
+        each(n, heads, [&](int i, int h, int r) {
+            if (from[r] >= 0) v[h][i] = static_cast<const T*>(base)[(from[r] + h * head) * units + unit];
+        });
     }
+    __device__ __forceinline__ void store(void* base, const long long* from, const long long* to, int n, int heads,
+                                          long long head) {
+        each(n, heads, [&](int i, int h, int r) {
+            if (from[r] >= 0) static_cast<T*>(base)[(to[r] + h * head) * units + unit] = v[h][i];
+        });
+    }
+};
+
+// Rows of codes in 16-byte units, or 8-byte ones (d = 64 at 3 bits: 24 bytes).
+template <typename T, int N>
+__device__ __forceinline__ void move_codes(const Layer& y, const long long* from, const long long* to, int n, int heads,
+                                           long long row, long long head) {
+    Mover<T, N> k(y.k_bytes), v(y.v_bytes);
+    uint8_t* kc = y.k_codes + row * y.k_bytes;
+    uint8_t* vc = y.v_codes + row * y.v_bytes;
+    k.load(kc, from, n, heads, head);
+    v.load(vc, from, n, heads, head);
+    __syncthreads();
+    k.store(kc, from, to, n, heads, head);
+    v.store(vc, from, to, n, heads, head);
 }
 
-// One block per (layer, sequence, kv head): all the path's rows are read
-// before any is written, so the path may name the drafts in any order.
+// Block (sequence and group of heads, layer).  It is latency: a chain of
+// length, path, row and write; several heads a block share the chain's start
+// and keep more rows in flight.  (48 sequences x 32 layers x 8 heads, up to 64
+// rows of 116 bytes each: 67 us with a block per head and divisions, see
+// below for this form.)
+// SMALL: every layer's rows are of at most 64 bytes, in 16-byte units (the
+// larger rows' registers would cost the others their blocks per SM).
+template <bool SMALL>
 __global__ void __launch_bounds__(THREADS) commit_kernel(const __grid_constant__ Args a) {
-    __shared__ long long from[MAX_PATH], to[MAX_PATH];
+    __shared__ long long from[MAX_PATH], to[MAX_PATH];  // cache rows of head 0 (from: -1, a row that stays)
     __shared__ int bad;
-    int l = 0;
-    const int blk = static_cast<int>(blockIdx.x);
-    while (l + 1 < a.n_layers && blk >= a.layers[l + 1].row0) ++l;
-    const Layer& y = a.layers[l];
-    const int b = (blk - y.row0) / y.hkv, head = (blk - y.row0) % y.hkv;
-    const int tid = threadIdx.x;
+    const Layer& y = a.layers[blockIdx.y];
+    const int b = static_cast<int>(blockIdx.x) / a.groups, h0 = static_cast<int>(blockIdx.x) % a.groups * HEADS;
+    if (h0 >= y.hkv) return;
+    const int tid = threadIdx.x, heads = min(HEADS, y.hkv - h0);
     const int n = a.path_lens[b], base = a.base[b];
-    const long long room = a.table ? static_cast<long long>(a.max_blocks) * y.capacity : y.capacity;
+    const int p = tid < min(n, a.max_path) ? a.path[static_cast<size_t>(b) * a.max_path + tid] : 0;
+    const long long room = a.table ? static_cast<long long>(a.max_blocks) * a.capacity : a.capacity;
     const bool fits = n >= 0 && n <= a.max_path && base >= 0 && base + static_cast<long long>(n) <= room;
-    const bool first = a.advance && blk == y.row0 + b * y.hkv && l == 0;
+    const bool first = a.advance && h0 == 0 && blockIdx.y == 0;
     if (tid == 0) bad = fits ? 0 : TQ_DEVERR_POSITION;
     __syncthreads();
     if (fits && tid < n) {
-        const int p = a.path[static_cast<size_t>(b) * a.max_path + tid];
         if (p < 0 || p >= MAX_PATH || base + static_cast<long long>(p) >= room) {
             atomicOr(&bad, TQ_DEVERR_POSITION);
         } else {
             auto row = [&](int slot) -> long long {
-                if (!a.table) return (static_cast<long long>(b) * y.hkv + head) * y.capacity + slot;
-                const int pg = a.table[static_cast<size_t>(b) * a.max_blocks + slot / y.capacity];
-                if (pg < 0 || pg >= y.num_blocks) {
+                if (!a.table) return static_cast<long long>(b) * y.hkv * a.capacity + slot;
+                const int pg = a.table[static_cast<size_t>(b) * a.max_blocks + slot / a.capacity];
+                if (pg < 0 || pg >= a.num_blocks) {
                     atomicOr(&bad, TQ_DEVERR_PAGE);
                     return -1;
                 }
-                return (static_cast<long long>(pg) * y.hkv + head) * y.capacity + slot % y.capacity;
+                return static_cast<long long>(pg) * y.hkv * a.capacity + slot % a.capacity;
             };
             to[tid] = row(base + tid);
             from[tid] = p == tid ? -1 : row(base + p);  // (a row that is already in place is left alone)
@@ -114,25 +146,28 @@ __global__ void __launch_bounds__(THREADS) commit_kernel(const __grid_constant__
         return;
     }
     if (first && tid == 0 && a.new_lens) a.new_lens[b] = base + n;
-    Held<uint4, 4> kc, vc;
-    Held<uint16_t, 1> kn, vn, kg;
-    Held<uint32_t, 2> kq;
-    load_rows(kc, reinterpret_cast<const uint4*>(y.k_codes), from, y.k_units, n * y.k_units);
-    load_rows(vc, reinterpret_cast<const uint4*>(y.v_codes), from, y.v_units, n * y.v_units);
-    load_rows(kn, y.k_norms, from, 1, n);
-    load_rows(vn, y.v_norms, from, 1, n);
+    const long long head = a.capacity, row = h0 * head;  // rows between heads; the block's first head
+    Mover<uint16_t, 1> kn(2), vn(2), kg(2);
+    Mover<uint32_t, 2> kq(4 * y.qjl_words);
+    kn.load(y.k_norms + row, from, n, heads, head);
+    vn.load(y.v_norms + row, from, n, heads, head);
     if (y.qjl_words) {
-        load_rows(kq, y.k_qjl, from, y.qjl_words, n * y.qjl_words);
-        load_rows(kg, y.k_gamma, from, 1, n);
+        kq.load(y.k_qjl + row * y.qjl_words, from, n, heads, head);
+        kg.load(y.k_gamma + row, from, n, heads, head);
     }
-    __syncthreads();
-    store_rows(kc, reinterpret_cast<uint4*>(y.k_codes), from, to, y.k_units, n * y.k_units);
-    store_rows(vc, reinterpret_cast<uint4*>(y.v_codes), from, to, y.v_units, n * y.v_units);
-    store_rows(kn, y.k_norms, from, to, 1, n);
-    store_rows(vn, y.v_norms, from, to, 1, n);
+    // (the codes' barrier stands between these loads and their stores too)
+    if constexpr (SMALL) {
+        move_codes<uint4, 1>(y, from, to, n, heads, row, head);
+    } else if (((y.k_bytes | y.v_bytes) & 15) == 0) {
+        move_codes<uint4, 4>(y, from, to, n, heads, row, head);
+    } else {
+        move_codes<uint2, 2>(y, from, to, n, heads, row, head);
+    }
+    kn.store(y.k_norms + row, from, to, n, heads, head);
+    vn.store(y.v_norms + row, from, to, n, heads, head);
     if (y.qjl_words) {
-        store_rows(kq, y.k_qjl, from, to, y.qjl_words, n * y.qjl_words);
-        store_rows(kg, y.k_gamma, from, to, 1, n);
+        kq.store(y.k_qjl + row * y.qjl_words, from, to, n, heads, head);
+        kg.store(y.k_gamma + row, from, to, n, heads, head);
     }
 }
 
@@ -156,9 +191,9 @@ static tq_status commit(int32_t n_layers, const tq_params* params, const tq_cach
     }
     for (int at = 0; at < n_layers; at += LAYERS_PER_LAUNCH) {
         Args a{};
-        a.n_layers = n_layers - at < LAYERS_PER_LAUNCH ? n_layers - at : LAYERS_PER_LAUNCH;
-        long long blocks = 0;
-        for (int i = 0; i < a.n_layers; ++i) {
+        bool small = true;
+        const int count = n_layers - at < LAYERS_PER_LAUNCH ? n_layers - at : LAYERS_PER_LAUNCH;
+        for (int i = 0; i < count; ++i) {
             const tq_params& p = params[at + i];
             const tq_cache& c = caches[at + i];
             Layer& y = a.layers[i];
@@ -168,17 +203,18 @@ static tq_status commit(int32_t n_layers, const tq_params* params, const tq_cach
             y.v_norms = c.v_norms;
             y.k_qjl = reinterpret_cast<uint32_t*>(c.k_qjl);
             y.k_gamma = c.k_gamma;
-            y.k_units = vector_bytes(p.k_mode, p.k_bits, p.head_dim) / 16;
-            y.v_units = vector_bytes(p.v_mode, p.v_bits, p.head_dim) / 16;
+            y.k_bytes = vector_bytes(p.k_mode, p.k_bits, p.head_dim);
+            y.v_bytes = vector_bytes(p.v_mode, p.v_bits, p.head_dim);
             y.qjl_words = p.qjl_dims / 32;
+            small = small && y.k_bytes <= 64 && y.v_bytes <= 64 && ((y.k_bytes | y.v_bytes) & 15) == 0;
             y.hkv = p.num_kv_heads;
-            y.row0 = static_cast<int32_t>(blocks);
-            y.capacity = c.capacity;
-            y.num_blocks = c.batch;
-            blocks += static_cast<long long>(batch) * p.num_kv_heads;
-            if (blocks > INT32_MAX) return TQ_ERR_INVALID_ARG;
+            const int groups = (p.num_kv_heads + HEADS - 1) / HEADS;
+            if (groups > a.groups) a.groups = groups;
         }
+        if (static_cast<long long>(batch) * a.groups > INT32_MAX) return TQ_ERR_INVALID_ARG;
         a.batch = batch;
+        a.capacity = caches[0].capacity;
+        a.num_blocks = caches[0].batch;
         a.max_path = max_path;
         a.advance = at == 0;
         a.max_blocks = table ? table->max_blocks : 0;
@@ -188,7 +224,10 @@ static tq_status commit(int32_t n_layers, const tq_params* params, const tq_cach
         a.base = d_base_lens;
         a.new_lens = d_new_lens;
         a.err = d_error;
-        commit_kernel<<<static_cast<unsigned>(blocks), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a);
+        const dim3 grid(static_cast<unsigned>(batch) * a.groups, static_cast<unsigned>(count));
+        cudaStream_t cs = static_cast<cudaStream_t>(stream);
+        if (small) commit_kernel<true><<<grid, THREADS, 0, cs>>>(a);
+        else commit_kernel<false><<<grid, THREADS, 0, cs>>>(a);
         if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
     }
     return TQ_OK;

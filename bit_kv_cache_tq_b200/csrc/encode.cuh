@@ -328,23 +328,16 @@ inline void fill_side(QuantSide& s, int mode, int bits, int d, const tq_codebook
         if (n == 2) w = 1.0;  // (not a width the codebooks produce: one boundary, at zero)
         w *= 1.0 - 1e-6;
         bool ok = 1.0 / w < 62.5;
-        for (int idx = 0; ok && idx < 128; ++idx) {
-            const int c = idx < 64 ? idx : idx - 128;
+        for (int c = -64, j = 0; ok && c < 64; ++c) {  // (cells and boundaries ascend together)
             const double lo = (c - 0.5) * w, hi = (c + 0.5) * w;
-            uint32_t below = 0;
-            int inside = -1;
-            for (int j = 0; j < n - 1; ++j) {
-                const double t = cb->boundaries[j];
-                if (t < lo) ++below;
-                else if (t < hi) {
-                    if (inside >= 0) ok = false;  // two boundaries in a cell
-                    inside = j;
-                }
-            }
-            const float bnd = inside >= 0 ? static_cast<float>(cb->boundaries[inside] / w) : INFINITY;
+            while (j < n - 1 && cb->boundaries[j] < lo) ++j;
+            const uint32_t below = static_cast<uint32_t>(j);
+            const bool inside = j < n - 1 && cb->boundaries[j] < hi;
+            if (inside && j + 1 < n - 1 && cb->boundaries[j + 1] < hi) ok = false;  // two boundaries in a cell
+            const float bnd = inside ? static_cast<float>(cb->boundaries[j] / w) : INFINITY;
             uint32_t bits32;
             std::memcpy(&bits32, &bnd, 4);
-            s.grid[idx] = (bits32 & ~15u) | below;
+            s.grid[c & 127] = (bits32 & ~15u) | below;
         }
         if (ok) s.grid_inv_w = static_cast<float>(1.0 / w);
     }

@@ -26,6 +26,8 @@ struct Args {
     const int32_t* table;
     int max_blocks, block_size, num_blocks;
     uint32_t signs[8];
+    float scale[2];           // of the fp16 centroids
+    int copies_log2;          // copies of a code table
 };
 
 template <int DTYPE>
@@ -49,13 +51,217 @@ __device__ __forceinline__ void store8(void* base, size_t off, const float* x) {
     }
 }
 
-// Grid: (blocks, batch, side).  A vector on d/32 lanes, as the encoders.
+// ------------------------------------------------- turbo vectors, no sketch
+// The inverse rotation on the tensor cores: x = diag(s) H c n / sqrt(d) for 16
+// vectors a warp.  H is a Kronecker product over the bits of the channel
+// index, so the sum over four of them is one m16n8k16 product with a constant
+// +-1 operand (16 x 16, in four registers) and the other bits are butterflies
+// between a lane's own accumulators.  Channel bits, for a lane t = lane % 4:
+//   0, 1  element i of the lane's four operand values
+//   2     which half of the 8 codes it looked up (s)
+//   3, 4  the lane t
+//   5 ..  its group of 8 channels (j)
+// The product runs over bits 0, 1, 3, 4; s and j are butterflies; the result's
+// fragment gives lane t the channels 32 j + 8 t .. + 7, whole 16-byte stores.
+// Centroids are fp16 at the codebook's scale (2^-11 at most); fp32 outputs add
+// a second term with what the rounding left.  It moves 2.4 KB for 16 vectors
+// at 4 bits to bf16 and issues about 350 instructions a warp, against 800 with
+// the butterflies in lanes and shuffles.
+constexpr int THREADS = 256;
+
+template <int BITS, bool LO>
+struct Table {
+    // Pairs of codes to pairs of fp16 centroids (and their remainders), a copy
+    // for every lane: lookups of a warp never share a bank.
+    uint32_t hi[1 << (2 * BITS)][32];
+    uint32_t lo[LO ? 1 << (2 * BITS) : 1][32];
+};
+
+template <int D, int DTYPE, int BITS>
+__device__ __forceinline__ void read_turbo(const Args& a, int side) {
+    constexpr bool LO = DTYPE == 0;
+    constexpr int J = D / 32;  // groups of 8 channels of a lane
+    extern __shared__ __align__(16) uint8_t rb_smem[];
+    Table<BITS, LO>& tab = *reinterpret_cast<Table<BITS, LO>*>(rb_smem);
+    const QuantSide& s = a.side[side];
+    void* out = a.out[side];
+    // (blocks with little to do make four copies: their lookups may collide)
+    const int copies = 1 << a.copies_log2;
+    for (int i = threadIdx.x; i < copies << (2 * BITS); i += THREADS) {
+        const int e = i >> a.copies_log2, l = i & (copies - 1);
+        const float c0 = s.centroids[e & ((1 << BITS) - 1)] * a.scale[side], c1 = s.centroids[e >> BITS] * a.scale[side];
+        const uint32_t h = ptx::pack_half2(c0, c1);
+        tab.hi[e][l] = h;
+        if constexpr (LO) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            tab.lo[e][l] = ptx::pack_half2(c0 - f.x, c1 - f.y);
+        }
+    }
+    __syncthreads();
+    const int b = static_cast<int>(blockIdx.y);
+    const int start = a.starts[b], count = a.counts[b];
+    if (start < 0 || count < 0 || count > a.max_count || start > a.capacity - count) {
+        if (a.err && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_POSITION);
+        return;
+    }
+    const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2, copy = lane & (copies - 1);
+    // +-1 operand: row k (a lane's element: k = 2 t + i, or 2 t + 8 + i - 2),
+    // column n: bit 0 of n is channel bit 0, bits 1, 2 are 3, 4, the tile is bit 1
+    uint32_t hb[2][2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int kt = t, ki = 2 * q + e;  // the operand's lane and element
+                const int par = __popc((kt & (g >> 1)) ^ 0) + ((ki & 1) & (g & 1)) + ((ki >> 1) & nt);
+                w |= (par & 1 ? 0xBC00u : 0x3C00u) << (16 * e);
+            }
+            hb[nt][q] = w;
+        }
+    // signs of the lane's channels 32 j + 8 t + e, as bit 8 j + e
+    uint32_t sg[(J + 3) / 4] = {};
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sg[j / 4] |= sign_bit(a.signs, 32 * j + 8 * t + e) << (8 * (j % 4) + e);
+    const float factor = rsqrtf(static_cast<float>(D)) / a.scale[side];
+    const int runs = (count + 15) / 16, tiles = runs * a.hkv;
+    const int nwarps = gridDim.x * (THREADS / 32);
+    size_t h = 0;
+    int t0 = 0;
+    bool ok[2];
+    uint16_t nraw[2];
+    uint32_t lo[2][J], hi[2][BITS == 3 ? J : 1];  // the lane's codes of group j (3 bits: in two words)
+    auto fetch = [&](int w) {  // 16 tokens of one head
+        const int hw = w / runs;
+        h = hw;
+        t0 = (w - hw * runs) * 16;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int tok = t0 + g + 8 * r;
+            ok[r] = tok < count;
+            size_t slot = (static_cast<size_t>(b) * a.hkv + h) * a.capacity + start + (ok[r] ? tok : 0);
+            if (a.table) {
+                const int at = start + (ok[r] ? tok : 0);
+                const int blk = a.table[static_cast<size_t>(b) * a.max_blocks + at / a.block_size];
+                if (blk < 0 || blk >= a.num_blocks) {
+                    if (ok[r] && a.err && t == 0) atomicOr(a.err, TQ_DEVERR_PAGE);
+                    ok[r] = false;
+                }
+                slot = (static_cast<size_t>(ok[r] ? blk : 0) * a.hkv + h) * a.block_size + at % a.block_size;
+            }
+            const uint8_t* row = s.codes + slot * (D * BITS / 8);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if constexpr (BITS == 4) {
+                    lo[r][j] = __ldg(reinterpret_cast<const uint32_t*>(row) + 4 * j + t);
+                } else if constexpr (BITS == 2) {
+                    lo[r][j] = __ldg(reinterpret_cast<const uint16_t*>(row) + 4 * j + t);
+                } else {  // 24 bits from byte 3 (4 j + t)
+                    const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + 3 * j;
+                    const int first = (3 * t) >> 2;
+                    lo[r][j] = __ldg(p + first);
+                    hi[r][j] = __ldg(p + (t == 3 ? 2 : first + (t > 0)));
+                }
+            }
+            nraw[r] = s.norms[slot];
+        }
+    };
+    int w = blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
+    for (; w < tiles; w += nwarps) {
+        fetch(w);
+        float norm[2];
+        bool live[2];
+        uint32_t code[2][J];  // the 8 codes of group j, from bit 0
+        size_t dst[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            live[r] = ok[r];
+            norm[r] = ok[r] ? half_bits_to_float(nraw[r]) * factor : 0.f;
+            dst[r] = ((static_cast<size_t>(b) * a.max_count + t0 + g + 8 * r) * a.hkv + h) * D + 8 * t;
+#pragma unroll
+            for (int j = 0; j < J; ++j) code[r][j] = BITS == 3 ? __funnelshift_r(lo[r][j], hi[r][BITS == 3 ? j : 0], 24 * t) : lo[r][j];
+        }
+        // acc[j][s]: channels 32 j + 8 t' + 4 s + .. before the butterflies
+        float acc[J][2][2][4];
+        constexpr uint32_t M = (1u << (2 * BITS)) - 1u;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int sx = 0; sx < 2; ++sx) {
+                // (rows g and g + 8) x (codes 0, 1 and 2, 3 of the half)
+                uint32_t f[4];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    f[q] = (code[q][j] >> (4 * BITS * sx)) & M;
+                    f[2 + q] = (code[q][j] >> (4 * BITS * sx + 2 * BITS)) & M;
+                }
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[j][sx][nt][q] = 0.f;
+                {
+                    const uint32_t x0 = tab.hi[f[0]][copy], x1 = tab.hi[f[1]][copy], x2 = tab.hi[f[2]][copy],
+                                   x3 = tab.hi[f[3]][copy];
+                    ptx::mma_16816(acc[j][sx][0], x0, x1, x2, x3, hb[0][0], hb[0][1]);
+                    ptx::mma_16816(acc[j][sx][1], x0, x1, x2, x3, hb[1][0], hb[1][1]);
+                }
+                if constexpr (LO) {
+                    const uint32_t x0 = tab.lo[f[0]][copy], x1 = tab.lo[f[1]][copy], x2 = tab.lo[f[2]][copy],
+                                   x3 = tab.lo[f[3]][copy];
+                    ptx::mma_16816(acc[j][sx][0], x0, x1, x2, x3, hb[0][0], hb[0][1]);
+                    ptx::mma_16816(acc[j][sx][1], x0, x1, x2, x3, hb[1][0], hb[1][1]);
+                }
+            }
+        // butterflies over s and the bits of j
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+                float2 v[2 * J];
+#pragma unroll
+                for (int k = 0; k < 2 * J; ++k) v[k] = make_float2(acc[k >> 1][k & 1][nt][q], acc[k >> 1][k & 1][nt][q + 1]);
+#pragma unroll
+                for (int m = 1; m < 2 * J; m <<= 1)
+#pragma unroll
+                    for (int k = 0; k < 2 * J; ++k)
+                        if (!(k & m)) {
+                            const float2 x = v[k], y = v[k + m];
+                            v[k] = ptx::fadd2(x, y);
+                            v[k + m] = ptx::fsub2(x, y);
+                        }
+#pragma unroll
+                for (int k = 0; k < 2 * J; ++k) {
+                    acc[k >> 1][k & 1][nt][q] = v[k].x;
+                    acc[k >> 1][k & 1][nt][q + 1] = v[k].y;
+                }
+            }
+        // lane t of row g + 8 r: channels 32 j + 8 t + (4 s + 2 nt + e)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[e] = flip_sign(acc[j][e >> 2][(e >> 1) & 1][2 * r + (e & 1)] * norm[r],
+                                     (sg[j / 4] >> (8 * (j % 4) + e)) & 1u);
+                if (live[r]) store8<DTYPE>(out, dst[r] + 32 * j, x);
+            }
+        }
+    }
+}
+
+// ------------------------------------------- int8 sides and sketched keys
+// A vector on d/32 lanes, as the encoders.
 template <int D, int DTYPE>
-__global__ void __launch_bounds__(256) read_back_kernel(const __grid_constant__ Args a) {
+__device__ __forceinline__ void read_other(const Args& a, int side) {
     constexpr int LPV = D / 32, VPW = 32 / LPV;
-    const QuantSide& s = a.side[blockIdx.z];
-    void* out = a.out[blockIdx.z];
-    if (!out) return;  // (the whole block: one side per block)
+    const QuantSide& s = a.side[side];
+    void* out = a.out[side];
     __shared__ float scen[16];
     if (threadIdx.x < 16) scen[threadIdx.x] = s.centroids[threadIdx.x];
     __syncthreads();
@@ -139,13 +345,58 @@ __global__ void __launch_bounds__(256) read_back_kernel(const __grid_constant__ 
     }
 }
 
-template <int D>
-static void launch(const Args& a, int dtype, dim3 grid, cudaStream_t s) {
-    switch (dtype) {
-        case TQ_F32: read_back_kernel<D, 0><<<grid, 256, 0, s>>>(a); break;
-        case TQ_BF16: read_back_kernel<D, 1><<<grid, 256, 0, s>>>(a); break;
-        default: read_back_kernel<D, 2><<<grid, 256, 0, s>>>(a); break;
+// Grid: (blocks, batch, side).
+template <int D, int DTYPE>
+__global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 2) read_back_kernel(const __grid_constant__ Args a) {
+    const int side = static_cast<int>(blockIdx.z);
+    const QuantSide& s = a.side[side];
+    if (!a.out[side]) return;
+    if (s.mode != TQ_MODE_TURBO || s.m > 0) read_other<D, DTYPE>(a, side);
+    else if (s.bits == 4) read_turbo<D, DTYPE, 4>(a, side);
+    else if (s.bits == 3) read_turbo<D, DTYPE, 3>(a, side);
+    else read_turbo<D, DTYPE, 2>(a, side);
+}
+
+template <int D, int DTYPE>
+static cudaError_t launch_typed(Args& a, int sms, cudaStream_t s) {
+    int bytes = 0;
+    for (int side = 0; side < 2; ++side) {
+        const QuantSide& q = a.side[side];
+        if (!a.out[side] || q.mode != TQ_MODE_TURBO || q.m > 0) continue;
+        const int n = static_cast<int>(q.bits == 4   ? sizeof(Table<4, DTYPE == 0>)
+                                       : q.bits == 3 ? sizeof(Table<3, DTYPE == 0>)
+                                                     : sizeof(Table<2, DTYPE == 0>));
+        if (n > bytes) bytes = n;
     }
+    const cudaError_t e =
+        cudaFuncSetAttribute(read_back_kernel<D, DTYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    // eight warps a block and 16 vectors a warp, two blocks an SM and side, shared by the sequences
+    const long long want = (static_cast<long long>((a.max_count + 15) / 16) * a.hkv + 7) / 8;
+    const long long most = (2ll * sms + a.batch - 1) / a.batch;
+    const dim3 grid(static_cast<unsigned>(want < most ? want : most), static_cast<unsigned>(a.batch), 2);
+    a.copies_log2 = want <= most ? 2 : 5;
+    read_back_kernel<D, DTYPE><<<grid, THREADS, bytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch(Args& a, int dtype, int sms, cudaStream_t s) {
+    switch (dtype) {
+        case TQ_F32: return launch_typed<D, 0>(a, sms, s);
+        case TQ_BF16: return launch_typed<D, 1>(a, sms, s);
+        default: return launch_typed<D, 2>(a, sms, s);
+    }
+}
+
+// One side's kernel arguments (no code grid: nothing is encoded here).
+static void fill(QuantSide& s, float& scale, int mode, int bits, int d, const tq_codebook* cb) {
+    s.mode = mode;
+    s.bits = mode == TQ_MODE_INT8 ? 8 : bits;
+    s.vbytes = vector_bytes(mode, bits, d);
+    if (mode != TQ_MODE_TURBO) return;
+    for (int j = 0; j < 1 << bits; ++j) s.centroids[j] = static_cast<float>(cb->centroids[j]);
+    scale = static_cast<float>(cb->fp16_scale > 0.0 ? cb->fp16_scale : std::sqrt(static_cast<double>(d)));
 }
 
 static tq_status read(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const tq_cache* cache,
@@ -161,8 +412,8 @@ static tq_status read(const tq_params* params, const tq_codebook* kcb, const tq_
     if (k_out && p.k_mode == TQ_MODE_TURBO && (st = validate_codebook(kcb, p.head_dim, p.k_bits)) != TQ_OK) return st;
     if (v_out && p.v_mode == TQ_MODE_TURBO && (st = validate_codebook(vcb, p.head_dim, p.v_bits)) != TQ_OK) return st;
     Args a{};
-    if (k_out) fill_side(a.side[0], p.k_mode, p.k_bits, p.head_dim, kcb);
-    if (v_out) fill_side(a.side[1], p.v_mode, p.v_bits, p.head_dim, vcb);
+    if (k_out) fill(a.side[0], a.scale[0], p.k_mode, p.k_bits, p.head_dim, kcb);
+    if (v_out) fill(a.side[1], a.scale[1], p.v_mode, p.v_bits, p.head_dim, vcb);
     a.side[0].codes = cache->k_codes;
     a.side[0].norms = cache->k_norms;
     a.side[0].qjl = cache->k_qjl;
@@ -188,18 +439,16 @@ static tq_status read(const tq_params* params, const tq_codebook* kcb, const tq_
     }
     if (a.batch > 65535) return TQ_ERR_INVALID_ARG;
     rotation_sign_bits(p.seed, p.head_dim, a.signs);
-    const long long warps = (static_cast<long long>(max_count) * p.num_kv_heads * (p.head_dim / 32) + 31) / 32;
-    long long blocks = (warps + 7) / 8;
-    const long long cap = (148ll * 8 + a.batch - 1) / a.batch;
-    if (blocks > cap) blocks = cap;
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(a.batch), 2);
+    const int sms = num_sms_current();
+    if (sms <= 0) return TQ_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
     switch (p.head_dim) {
-        case 64: launch<64>(a, dtype, grid, s); break;
-        case 128: launch<128>(a, dtype, grid, s); break;
-        default: launch<256>(a, dtype, grid, s); break;
+        case 64: e = launch<64>(a, dtype, sms, s); break;
+        case 128: e = launch<128>(a, dtype, sms, s); break;
+        default: e = launch<256>(a, dtype, sms, s); break;
     }
-    return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+    return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 }  // namespace read_back

@@ -38,7 +38,7 @@ struct Args {
     const int32_t* rope_positions;  // [batch][n_new], or null: the slot
     uint32_t* err;
     int tokens, n_new, hq, hkv, capacity;
-    int chunk, chunks;            // tokens per block, blocks per kind
+    int chunk, chunks, kinds;     // tokens per block, blocks per kind, kinds (3, or 2 without queries)
     uint64_t hq_magic, hkv_magic, n_new_magic;
     const int32_t* table;
     int max_blocks, block_size, num_blocks;
@@ -116,6 +116,39 @@ __device__ __forceinline__ void turn(const Args& a, const float2* cs, const void
     }
 }
 
+// A lane's 32 coordinates as they are in memory.
+template <int D, int DTYPE>
+struct Raw {
+    static constexpr int LPV = D / 32, N = DTYPE == 0 ? 2 : 1;
+    uint4 w[4 * N];
+    __device__ __forceinline__ void load(const void* src, size_t off, int sub) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + off * (DTYPE == 0 ? 4 : 2));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[N * k + i] = __ldcs(p + N * (sub + LPV * k) + i);
+    }
+    __device__ __forceinline__ void values(float (&x)[32]) const {
+#pragma unroll
+        for (int k = 0; k < 4 * N; ++k) {
+            const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DTYPE == 0) {
+                    x[4 * k + i] = __uint_as_float(u[i]);
+                } else if constexpr (DTYPE == 1) {  // bf16: the upper half of an fp32
+                    x[8 * k + 2 * i] = __uint_as_float(u[i] << 16);
+                    x[8 * k + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+                    x[8 * k + 2 * i] = f.x;
+                    x[8 * k + 2 * i + 1] = f.y;
+                }
+            }
+        }
+    }
+};
+
 template <int DTYPE>
 __device__ __forceinline__ void store8(void* base, size_t off, const float* x) {
     if constexpr (DTYPE == 0) {
@@ -146,8 +179,25 @@ __device__ __forceinline__ void run_kind(const Args& a, Shared<D>& sh, int chunk
     const int tid = threadIdx.x;
     if (grid_path && tid < 128) sh.grid[tid] = s.grid[tid];
     const int tok0 = chunk * a.chunk, ntok = min(a.chunk, a.tokens - tok0);
+    const int lane = tid & 31, sub = lane % LPV, grp = lane / LPV;
+    const int heads = KIND == 2 ? a.hq : a.hkv;
+    const uint64_t magic = KIND == 2 ? a.hq_magic : a.hkv_magic;
+    const void* src = a.src[KIND == 2 ? 2 : KIND];
+    const long long stride = a.stride[KIND == 2 ? 2 : KIND];
+    const uint32_t total = static_cast<uint32_t>(ntok) * heads;
     ptx::wait_prerequisites();
     ptx::launch_dependents();  // (after the wait, as the append kernel does: see quantize_side)
+    // the first vectors are on their way while the table is made, and the next
+    // queries while a pass's are turned
+    Raw<D, DTYPE> raw;
+    auto fetch = [&](uint32_t v) {
+        if (v < total) {
+            const uint32_t t = div_magic(v, magic), h = v - t * heads;
+            raw.load(src, static_cast<size_t>(tok0 + t) * stride + static_cast<size_t>(h) * D, sub);
+        }
+    };
+    uint32_t base = (tid / 32) * VPW;
+    fetch(base + grp);
     // positions, slots, cosines and sines of the block's tokens
     if (KIND < 2 && tid < ntok) {
         const uint32_t tok = static_cast<uint32_t>(tok0 + tid), b = div_magic(tok, a.n_new_magic);
@@ -185,27 +235,22 @@ __device__ __forceinline__ void run_kind(const Args& a, Shared<D>& sh, int chunk
         }
     }
     __syncthreads();
-    const int lane = tid & 31, sub = lane % LPV, grp = lane / LPV;
-    const int heads = KIND == 2 ? a.hq : a.hkv;
-    const uint64_t magic = KIND == 2 ? a.hq_magic : a.hkv_magic;
     const uint32_t smask = KIND < 2 ? lane_sign_mask<D>(a.signs, sub) : 0u;
     const long long hstride = a.table ? a.block_size : a.capacity;  // cache rows between heads
-    const void* src = a.src[KIND == 2 ? 2 : KIND];
-    const long long stride = a.stride[KIND == 2 ? 2 : KIND];
-    const uint32_t total = static_cast<uint32_t>(ntok) * heads;
-    for (uint32_t base = (tid / 32) * VPW; base < total; base += WARPS * VPW) {
+    for (; base < total; base += WARPS * VPW) {
         const uint32_t v = base + grp;
         const bool in = v < total;
         const uint32_t t = in ? div_magic(v, magic) : 0u, h = in ? v - t * heads : 0u;
         const size_t off = static_cast<size_t>(tok0 + t) * stride + static_cast<size_t>(h) * D;
         float x[32];
         if (in) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) load8_stream<DTYPE>(src, off + 8 * (sub + LPV * k), &x[8 * k]);
+            raw.values(x);
         } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = 0.0f;
         }
+        // (the encoders need the registers)
+        if (KIND == 2 && base + WARPS * VPW < total) fetch(v + WARPS * VPW);
         if (KIND != 1 && in) turn<D, DTYPE>(a, sh.cs[t], src, off, x, sub);
         if constexpr (KIND == 2) {
             // (the output may be the input: every lane of the vector has read it before any writes)
@@ -235,6 +280,7 @@ __device__ __forceinline__ void run_kind(const Args& a, Shared<D>& sh, int chunk
             } else {
                 turbo_encode<D, 2>(s, x, sub, slot, valid, smask);
             }
+            if (base + WARPS * VPW < total) fetch(v + WARPS * VPW);
         }
     }
 }
@@ -242,16 +288,17 @@ __device__ __forceinline__ void run_kind(const Args& a, Shared<D>& sh, int chunk
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(THREADS, 3) rope_append_kernel(const __grid_constant__ Args a) {
     __shared__ Shared<D> sh;
-    const int kind = static_cast<int>(blockIdx.x) / a.chunks, chunk = static_cast<int>(blockIdx.x) % a.chunks;
+    // (the kinds alternate: encoding is bound by instructions, turning queries by memory)
+    const int kind = static_cast<int>(blockIdx.x) % a.kinds, chunk = static_cast<int>(blockIdx.x) / a.kinds;
     if (kind == 0) run_kind<D, DTYPE, 0>(a, sh, chunk);
     else if (kind == 1) run_kind<D, DTYPE, 1>(a, sh, chunk);
     else run_kind<D, DTYPE, 2>(a, sh, chunk);
 }
 
 template <int D, int DTYPE>
-static cudaError_t launch(const Args& a, bool queries, cudaStream_t stream) {
+static cudaError_t launch(const Args& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.chunks) * (queries ? 3u : 2u));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.chunks) * a.kinds);
     cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -264,11 +311,11 @@ static cudaError_t launch(const Args& a, bool queries, cudaStream_t stream) {
 }
 
 template <int D>
-static cudaError_t launch_dtype(const Args& a, int dtype, bool queries, cudaStream_t stream) {
+static cudaError_t launch_dtype(const Args& a, int dtype, cudaStream_t stream) {
     switch (dtype) {
-        case TQ_F32: return launch<D, 0>(a, queries, stream);
-        case TQ_BF16: return launch<D, 1>(a, queries, stream);
-        default: return launch<D, 2>(a, queries, stream);
+        case TQ_F32: return launch<D, 0>(a, stream);
+        case TQ_BF16: return launch<D, 1>(a, stream);
+        default: return launch<D, 2>(a, stream);
     }
 }
 
@@ -342,6 +389,7 @@ static tq_status append(const tq_params* params, const tq_codebook* kcb, const t
     a.capacity = capacity;
     a.chunk = tokens_per_block(tokens, sms);
     a.chunks = (a.tokens + a.chunk - 1) / a.chunk;
+    a.kinds = q ? 3 : 2;
     a.hq_magic = quotient_magic(static_cast<uint32_t>(p.num_q_heads));
     a.hkv_magic = quotient_magic(static_cast<uint32_t>(p.num_kv_heads));
     a.n_new_magic = quotient_magic(static_cast<uint32_t>(n_new));
@@ -359,9 +407,9 @@ static tq_status append(const tq_params* params, const tq_codebook* kcb, const t
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (p.head_dim) {
-        case 64: e = launch_dtype<64>(a, dtype, q != nullptr, s); break;
-        case 128: e = launch_dtype<128>(a, dtype, q != nullptr, s); break;
-        default: e = launch_dtype<256>(a, dtype, q != nullptr, s); break;
+        case 64: e = launch_dtype<64>(a, dtype, s); break;
+        case 128: e = launch_dtype<128>(a, dtype, s); break;
+        default: e = launch_dtype<256>(a, dtype, s); break;
     }
     return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }

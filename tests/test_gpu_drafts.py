@@ -405,7 +405,7 @@ def test_commit_drafts(page, order):
     """Layers of different heads, widths and modes; paths of 0 .. 64 drafts, in ascending or any order and with
     repeats; every byte of every cache, and the new lengths."""
     specs = [(128, 8, 4, 2, 0), (128, 2, 3, 3, 64), (64, 3, 8, 8, 0), (256, 1, 8, 4, 0), (256, 2, 2, 2, 256),
-             (128, 1, 2, 8, 32)]
+             (128, 1, 2, 8, 32), (64, 5, 3, 3, 0), (64, 6, 3, 4, 32), (256, 9, 3, 8, 0)]
     batch, n = 5, 64
     layers, table = _commit_layers(specs, batch, 150, page, seed=3)
     rng = np.random.default_rng(1)
