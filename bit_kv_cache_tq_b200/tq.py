@@ -423,6 +423,42 @@ def tq_append_decode_attention_paged(params, kcb, vcb, k_new, v_new, q, pool, ta
 
 
 # ------------------------------------------------ drafted tokens, rotary positions
+# (These calls sit between a decoding loop's kernels of a few microseconds, so
+# their marshalling is kept short: addresses as plain integers, no objects.)
+_CODES = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_for(t, stream):
+    """The stream's handle; t is one of the call's tensors, which lie on the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    device = t.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError("the tensors are on device %d, the current device is %d"
+                         % (device, torch.cuda.current_device()))
+    return _raw_stream(device) if _raw_stream else torch.cuda.current_stream().cuda_stream
+
+
+def _cache_ref(cache):
+    return ctypes.byref(tq_cache(cache.batch, cache.capacity, cache.k_codes.data_ptr(), cache.k_norms.data_ptr(),
+                                 _address(cache.k_qjl), _address(cache.k_gamma), cache.v_codes.data_ptr(),
+                                 cache.v_norms.data_ptr(), _address(cache.qjl_matrix)))
+
+
+def _check_int32(t, n, name):
+    if not (t.dtype is torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == n):
+        raise ValueError("%s: a contiguous int32 CUDA tensor of %d elements is wanted" % (name, n))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
 def tq_rope_init(rotary_dims, layout=TQ_ROPE_HALF, base=10000.0, scaling=TQ_ROPE_SCALE_NONE, factor=1.0, low=1.0,
                  high=4.0, trained_len=8192.0, magnitude=0.0):
     """A layer's rotary table (see include/tq.h for the scalings)."""
@@ -433,8 +469,10 @@ def tq_rope_init(rotary_dims, layout=TQ_ROPE_HALF, base=10000.0, scaling=TQ_ROPE
 
 
 def _token_stride(t, name):
-    """Elements between tokens of t [batch, n, heads, d]: heads and channels contiguous, tokens evenly spaced over the
-    whole batch (a slice of a projection's output qualifies)."""
+    """Elements between tokens of t [batch, n, heads, d], 0 for a contiguous tensor: heads and channels contiguous,
+    tokens evenly spaced over the whole batch (a slice of a projection's output qualifies)."""
+    if t.is_contiguous():
+        return 0
     b, n, h, d = t.shape
     row = t.stride(1) if n > 1 else t.stride(0) if b > 1 else h * d
     if (row < h * d or (d > 1 and t.stride(3) != 1) or (h > 1 and t.stride(2) != d)
@@ -443,42 +481,44 @@ def _token_stride(t, name):
     return row
 
 
-def _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, q_out, rope_positions):
-    assert k_new.dtype == v_new.dtype and k_new.shape == v_new.shape and k_new.shape[2] == params.num_kv_heads
-    assert k_new.shape[3] == params.head_dim and positions.dtype == torch.int32 and positions.is_cuda
-    assert positions.is_contiguous() and positions.numel() == k_new.shape[0]
-    assert (q is None) == (q_out is None)
+def _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, batch, q_out, rope_positions):
+    shape = k_new.shape
+    if shape != v_new.shape or len(shape) != 4 or shape[0] != batch or shape[2] != params.num_kv_heads or (
+            shape[3] != params.head_dim or k_new.dtype is not v_new.dtype):
+        raise ValueError("k_new, v_new: [batch, n_new, num_kv_heads, head_dim] of one type are wanted")
+    _check_int32(positions, batch, "positions")
     stride = 0
     if q is not None:
-        assert q.dtype == k_new.dtype and q_out.dtype == q.dtype and q_out.shape == q.shape and q_out.is_contiguous()
-        assert q.shape == k_new.shape[:2] + (params.num_q_heads, params.head_dim)
+        if q.shape != (batch, shape[1], params.num_q_heads, shape[3]) or q.dtype is not k_new.dtype:
+            raise ValueError("q: [batch, n_new, num_q_heads, head_dim] of the keys' type is wanted")
+        if q_out is None or q_out.shape != q.shape or q_out.dtype is not q.dtype or not q_out.is_contiguous():
+            raise ValueError("q_out: a contiguous tensor like q is wanted")
         stride = _token_stride(q, "q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
     if rope_positions is not None:
-        assert rope_positions.dtype == torch.int32 and rope_positions.is_cuda and rope_positions.is_contiguous()
-        assert rope_positions.shape == k_new.shape[:2]
-    return (ctypes.byref(params), kcb and ctypes.byref(kcb), vcb and ctypes.byref(vcb), ctypes.byref(rope), _ptr(q),
-            stride, _ptr(k_new), _token_stride(k_new, "k_new"), _ptr(v_new), _token_stride(v_new, "v_new"),
-            _dtype_code(k_new), k_new.shape[1], _ptr(positions), _ptr(rope_positions), ctypes.byref(cache.struct()))
+        _check_int32(rope_positions, batch * shape[1], "rope_positions")
+    return (ctypes.byref(params), _ref(kcb), _ref(vcb), ctypes.byref(rope), _address(q), stride, k_new.data_ptr(),
+            _token_stride(k_new, "k_new"), v_new.data_ptr(), _token_stride(v_new, "v_new"), _CODES[k_new.dtype],
+            shape[1], positions.data_ptr(), _address(rope_positions), _cache_ref(cache))
 
 
 def tq_rope_append(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, q_out, rope_positions=None, error=None,
                    stream=None):
     """Turn q ([batch, n_new, Hq, d]) into q_out and append k_new (turned) and v_new ([batch, n_new, Hkv, d]) at slots
     positions[b] ..; rope_positions: int32 [batch, n_new] or None (the slots).  q, k_new and v_new may be slices of one
-    projection's output; q and q_out may be None, or the same tensor."""
-    assert positions.numel() == cache.batch
-    args = _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, q_out, rope_positions)
-    _check(_lib.tq_rope_append(*args, _ptr(q_out), _ptr(error), _stream(stream)), "tq_rope_append")
+    projection's output; q and q_out may be None, or the same contiguous tensor."""
+    args = _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, cache.batch, q_out, rope_positions)
+    _check(_lib.tq_rope_append(*args, _address(q_out), _address(error), _stream_for(k_new, stream)), "tq_rope_append")
 
 
 def tq_rope_append_paged(params, kcb, vcb, rope, q, k_new, v_new, positions, pool, table, q_out, rope_positions=None,
                          error=None, stream=None):
     """tq_rope_append on a paged cache (see tq_quantize_append_paged)."""
     bt = block_table(table)
-    assert positions.numel() == bt.batch
-    args = _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, pool, q_out, rope_positions)
-    _check(_lib.tq_rope_append_paged(*args, ctypes.byref(bt), _ptr(q_out), _ptr(error), _stream(stream)),
-           "tq_rope_append_paged")
+    args = _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, pool, bt.batch, q_out, rope_positions)
+    _check(_lib.tq_rope_append_paged(*args, ctypes.byref(bt), _address(q_out), _address(error),
+                                     _stream_for(k_new, stream)), "tq_rope_append_paged")
 
 
 def tq_tree_workspace_bytes(params, batch, n_draft):
@@ -489,14 +529,20 @@ def tq_tree_workspace_bytes(params, batch, n_draft):
 
 
 def _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, cache, batch, out):
-    assert q.is_contiguous() and out.is_contiguous() and out.shape == q.shape
-    assert q.shape[0] == batch and q.shape[2] == params.num_q_heads and q.shape[3] == params.head_dim
-    assert tree_mask.dtype == torch.int64 and tree_mask.is_cuda and tree_mask.is_contiguous()
-    assert tree_mask.shape == q.shape[:2]
-    for t in (base_lens, draft_lens):
-        assert t is None or (t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == batch)
-    return (ctypes.byref(params), kcb and ctypes.byref(kcb), vcb and ctypes.byref(vcb), _ptr(q), _dtype_code(q),
-            q.shape[1], _ptr(tree_mask), _ptr(base_lens), _ptr(draft_lens), ctypes.byref(cache.struct()))
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != batch or shape[2] != params.num_q_heads or shape[3] != params.head_dim or (
+            not q.is_contiguous()):
+        raise ValueError("q: a contiguous [batch, n_draft, num_q_heads, head_dim] is wanted")
+    if out.shape != shape or not out.is_contiguous():
+        raise ValueError("out: a contiguous tensor of q's shape is wanted")
+    if not (tree_mask.dtype is torch.int64 and tree_mask.is_cuda and tree_mask.is_contiguous()
+            and tree_mask.shape == shape[:2]):
+        raise ValueError("tree_mask: a contiguous int64 CUDA tensor [batch, n_draft] is wanted")
+    _check_int32(base_lens, batch, "base_lens")
+    if draft_lens is not None:
+        _check_int32(draft_lens, batch, "draft_lens")
+    return (ctypes.byref(params), _ref(kcb), _ref(vcb), q.data_ptr(), _CODES[q.dtype], shape[1], tree_mask.data_ptr(),
+            base_lens.data_ptr(), _address(draft_lens), _cache_ref(cache))
 
 
 def tq_tree_attention(params, kcb, vcb, q, tree_mask, base_lens, cache, out, workspace, draft_lens=None, error=None,
@@ -505,9 +551,8 @@ def tq_tree_attention(params, kcb, vcb, q, tree_mask, base_lens, cache, out, wor
     drafts in the slots after them, those whose bits tree_mask (int64 [batch, n_draft]) has set; out: like q, in fp32,
     bf16 or fp16.  workspace: uint8, tq_tree_workspace_bytes(params, batch, n_draft), any contents."""
     args = _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, cache, cache.batch, out)
-    _check(_lib.tq_tree_attention(*args, _ptr(out), _dtype_code(out), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _ptr(error), _stream(stream)),
-           "tq_tree_attention")
+    _check(_lib.tq_tree_attention(*args, out.data_ptr(), _CODES[out.dtype], workspace.data_ptr(), workspace.nbytes,
+                                  _address(error), _stream_for(q, stream)), "tq_tree_attention")
 
 
 def tq_tree_attention_paged(params, kcb, vcb, q, tree_mask, base_lens, pool, table, out, workspace, draft_lens=None,
@@ -515,35 +560,39 @@ def tq_tree_attention_paged(params, kcb, vcb, q, tree_mask, base_lens, pool, tab
     """tq_tree_attention on a paged cache (see tq_quantize_append_paged)."""
     bt = block_table(table)
     args = _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, pool, bt.batch, out)
-    _check(_lib.tq_tree_attention_paged(*args, ctypes.byref(bt), _ptr(out), _dtype_code(out), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(), _ptr(error), _stream(stream)),
-           "tq_tree_attention_paged")
+    _check(_lib.tq_tree_attention_paged(*args, ctypes.byref(bt), out.data_ptr(), _CODES[out.dtype],
+                                        workspace.data_ptr(), workspace.nbytes, _address(error),
+                                        _stream_for(q, stream)), "tq_tree_attention_paged")
 
 
 class draft_layers:
     """The layers a commit moves drafts in, kept by the program between steps: [(params, CacheTensors), ...]."""
 
     def __init__(self, layers):
-        self.layers = list(layers)  # (keeps the tensors alive)
+        self.layers = list(layers)
+        self.tensors = [list(vars(c).values()) for _, c in self.layers]  # (whose addresses the structs hold)
         n = len(self.layers)
         self.params = (tq_params * n)(*[p for p, _ in self.layers])
         self.caches = (tq_cache * n)(*[c.struct() for _, c in self.layers])
 
 
 def _commit_call(path, path_lens, base_lens, new_lens, batch):
-    assert path.dtype == torch.int32 and path.is_cuda and path.is_contiguous() and path.dim() == 2
-    assert path.shape[0] == batch
-    for t in (path_lens, base_lens, new_lens):
-        assert t is None or (t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == batch)
-    return _ptr(path), path.shape[1], _ptr(path_lens), _ptr(base_lens), _ptr(new_lens)
+    if path.dim() != 2:
+        raise ValueError("path: [batch, max_path] is wanted")
+    _check_int32(path, batch * path.shape[1], "path")
+    _check_int32(path_lens, batch, "path_lens")
+    _check_int32(base_lens, batch, "base_lens")
+    if new_lens is not None:
+        _check_int32(new_lens, batch, "new_lens")
+    return path.data_ptr(), path.shape[1], path_lens.data_ptr(), base_lens.data_ptr(), _address(new_lens)
 
 
 def tq_commit_drafts(layers, path, path_lens, base_lens, new_lens=None, error=None, stream=None):
     """Move draft path[b, i] (int32 [batch, max_path]) to slot base_lens[b] + i, i < path_lens[b], in every layer of a
     draft_layers; new_lens: base_lens + path_lens."""
-    args = _commit_call(path, path_lens, base_lens, new_lens, layers.caches[0].batch if len(layers.layers) else 0)
-    _check(_lib.tq_commit_drafts(len(layers.layers), layers.params, layers.caches, *args, _ptr(error),
-                                 _stream(stream)), "tq_commit_drafts")
+    args = _commit_call(path, path_lens, base_lens, new_lens, layers.caches[0].batch)
+    _check(_lib.tq_commit_drafts(len(layers.layers), layers.params, layers.caches, *args, _address(error),
+                                 _stream_for(path, stream)), "tq_commit_drafts")
 
 
 def tq_commit_drafts_paged(layers, table, path, path_lens, base_lens, new_lens=None, error=None, stream=None):
@@ -551,24 +600,29 @@ def tq_commit_drafts_paged(layers, table, path, path_lens, base_lens, new_lens=N
     bt = block_table(table)
     args = _commit_call(path, path_lens, base_lens, new_lens, bt.batch)
     _check(_lib.tq_commit_drafts_paged(len(layers.layers), layers.params, layers.caches, ctypes.byref(bt), *args,
-                                       _ptr(error), _stream(stream)), "tq_commit_drafts_paged")
+                                       _address(error), _stream_for(path, stream)), "tq_commit_drafts_paged")
 
 
 def _read_call(params, starts, counts, batch, k_out, v_out):
-    outs = [t for t in (k_out, v_out) if t is not None]
-    assert outs and all(t.is_contiguous() and t.dtype == outs[0].dtype and t.shape == outs[0].shape for t in outs)
-    assert outs[0].shape[0] == batch and outs[0].shape[2:] == (params.num_kv_heads, params.head_dim)
-    for t in (starts, counts):
-        assert t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == batch
-    return _ptr(starts), _ptr(counts), outs[0].shape[1], _dtype_code(outs[0]), _ptr(k_out), _ptr(v_out)
+    out = v_out if k_out is None else k_out
+    shape = out.shape
+    if len(shape) != 4 or shape[0] != batch or shape[2] != params.num_kv_heads or shape[3] != params.head_dim or (
+            not out.is_contiguous()):
+        raise ValueError("outputs: contiguous [batch, max_count, num_kv_heads, head_dim] are wanted")
+    if k_out is not None and v_out is not None and (
+            v_out.shape != shape or v_out.dtype is not k_out.dtype or not v_out.is_contiguous()):
+        raise ValueError("k_out and v_out must be alike")
+    _check_int32(starts, batch, "starts")
+    _check_int32(counts, batch, "counts")
+    return starts.data_ptr(), counts.data_ptr(), shape[1], _CODES[out.dtype], _address(k_out), _address(v_out)
 
 
 def tq_read_back(params, kcb, vcb, cache, starts, counts, k_out=None, v_out=None, error=None, stream=None):
     """Reconstruct slots starts[b] .. starts[b] + counts[b] - 1 of every sequence into k_out and v_out
     ([batch, max_count, Hkv, d], fp32, bf16 or fp16); rows past counts[b] are left as they are."""
     args = _read_call(params, starts, counts, cache.batch, k_out, v_out)
-    _check(_lib.tq_read_back(ctypes.byref(params), kcb and ctypes.byref(kcb), vcb and ctypes.byref(vcb),
-                             ctypes.byref(cache.struct()), *args, _ptr(error), _stream(stream)), "tq_read_back")
+    _check(_lib.tq_read_back(ctypes.byref(params), _ref(kcb), _ref(vcb), _cache_ref(cache), *args, _address(error),
+                             _stream_for(starts, stream)), "tq_read_back")
 
 
 def tq_read_back_paged(params, kcb, vcb, pool, table, starts, counts, k_out=None, v_out=None, error=None,
@@ -576,9 +630,8 @@ def tq_read_back_paged(params, kcb, vcb, pool, table, starts, counts, k_out=None
     """tq_read_back on a paged cache (see tq_quantize_append_paged)."""
     bt = block_table(table)
     args = _read_call(params, starts, counts, bt.batch, k_out, v_out)
-    _check(_lib.tq_read_back_paged(ctypes.byref(params), kcb and ctypes.byref(kcb), vcb and ctypes.byref(vcb),
-                                   ctypes.byref(pool.struct()), ctypes.byref(bt), *args, _ptr(error),
-                                   _stream(stream)), "tq_read_back_paged")
+    _check(_lib.tq_read_back_paged(ctypes.byref(params), _ref(kcb), _ref(vcb), _cache_ref(pool), ctypes.byref(bt),
+                                   *args, _address(error), _stream_for(starts, stream)), "tq_read_back_paged")
 
 
 def tq_read_device_error(error, stream=None, timeout_ms=2000):

@@ -209,9 +209,38 @@ def test_binding_finds_token_strides():
     qkv = torch.zeros(2, 5, 12 * 128)
     q = qkv[..., : 8 * 128].unflatten(-1, (-1, 128))
     assert tq._token_stride(q, "q") == 12 * 128
-    assert tq._token_stride(torch.zeros(2, 5, 8, 128), "q") == 8 * 128
-    assert tq._token_stride(torch.zeros(3, 1, 8, 128), "q") == 8 * 128
+    assert tq._token_stride(torch.zeros(2, 5, 8, 128), "q") == 0
+    assert tq._token_stride(qkv[:, :1, : 8 * 128].unflatten(-1, (-1, 128)), "q") == 5 * 12 * 128
     for bad in (torch.zeros(2, 8, 5, 128).transpose(1, 2), torch.zeros(2, 5, 8, 256)[..., ::2],
                 torch.zeros(2, 7, 8, 128)[:, :5], torch.zeros(1, 1, 8, 128).expand(3, 1, 8, 128)):
         with pytest.raises(ValueError):
             tq._token_stride(bad, "q")
+
+
+def _cpu_call():
+    p, kcb, vcb, _ = _setup()
+    u8 = torch.zeros(64, dtype=torch.uint8)
+    return p, kcb, vcb, tq.CacheTensors(2, 16, u8, u8, None, None, u8, u8, None), torch.zeros(2, dtype=torch.int32)
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    """Shapes, types and places are checked before the library is called."""
+    p, kcb, vcb, cache, i32 = _cpu_call()
+    k, q = torch.zeros(2, 3, 2, 128), torch.zeros(2, 3, 8, 128)
+    rope = tq.tq_rope_init(128)
+    for args in ((q, k, k, i32, cache, q), (q, k[:, :2], k, i32, cache, q), (q, k, k.half(), i32, cache, q),
+                 (q, k[:1], k[:1], i32, cache, q), (None, k, k, i32, cache, q)):
+        with pytest.raises(ValueError):
+            tq.tq_rope_append(p, kcb, vcb, rope, *args)
+    mask = torch.zeros(2, 3, dtype=torch.int64)
+    ws = torch.zeros(16, dtype=torch.uint8)
+    for args in ((q, mask, i32), (q[:, :2], mask, i32), (q.transpose(1, 2), mask, i32), (q, mask.int(), i32)):
+        with pytest.raises(ValueError):
+            tq.tq_tree_attention(p, kcb, vcb, *args, cache, q, ws)
+    path = torch.zeros(2, 4, dtype=torch.int32)
+    for bad in (path, path[0], path.long()):
+        with pytest.raises(ValueError):
+            tq.tq_commit_drafts(tq.draft_layers([(p, cache)]), bad, i32, i32)
+    for outs in ((k, k), (k, k.half()), (q, None), (None, k[:1])):
+        with pytest.raises(ValueError):
+            tq.tq_read_back(p, kcb, vcb, cache, i32, i32, *outs)
