@@ -15,7 +15,8 @@
 // The general kernel takes every configuration: 64 query rows (16 a warp) of
 // one (sequence, kv head) against tiles of BK keys, dequantised to fp16 in
 // shared memory; warp-level MMAs (m16n8k16, fp32 accumulation); the online
-// softmax in registers.  Queries enter as two fp16 terms, so a score keeps
+// softmax in registers; the next tile's packed rows are loaded while a tile is
+// worked on.  Queries enter as two fp16 terms, so a score keeps
 // about 22 bits of its query.  The key axis is split between blocks and the
 // merge kernel joins the pieces.
 
@@ -38,16 +39,106 @@ __host__ __device__ constexpr int gen_qk_stride(int d, int m) { return d + m + 8
 template <int D>
 constexpr size_t gen_smem(int m) {
     return (2ull * GEN_ROWS + GEN_BK<D>) * gen_qk_stride(D, m) * 2 + GEN_BK<D> * (D + 8) * 2ull +
-           GEN_BK<D> * 4ull + GEN_ROWS * 4ull + 128;
+           GEN_BK<D> * 8ull + 128;
 }
 
 __device__ __forceinline__ void ldmatrix_x2_trans(uint32_t& r0, uint32_t& r1, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
 }
 
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The general kernel's queries, once a call: rotated (turbo keys), times the
+// softmax scale in log2 units, the sketch's projections appended, as two fp16
+// terms: per unit [2][64 rows][d + m].  A row on d / 32 lanes; blockIdx.y
+// takes PREP_SKETCH of the sketch's rows (the first also the rotated row).
+constexpr int PREP_THREADS = 128, PREP_SKETCH = 8;
 template <int D>
-__global__ void __launch_bounds__(GEN_THREADS) tree_general_kernel(const __grid_constant__ Args a) {
-    constexpr int BK = GEN_BK<D>, LPV = D / 32, VPW = 32 / LPV;
+__global__ void __launch_bounds__(PREP_THREADS) tree_general_prep_kernel(const __grid_constant__ Args a) {
+    constexpr int LPV = D / 32, VPW = 32 / LPV;
+    ptx::wait_prerequisites();
+    ptx::launch_dependents();
+    const int lane = threadIdx.x & 31, sub = lane % LPV, m = a.qjl_dims, KD = D + m, G = a.group;
+    const long long row = (static_cast<long long>(blockIdx.x) * (PREP_THREADS / 32) + (threadIdx.x >> 5)) * VPW + lane / LPV;
+    const int u = static_cast<int>(row / GEN_ROWS), r = static_cast<int>(row % GEN_ROWS);
+    if (u >= a.units) return;  // (whole warps)
+    const int rt = r / G, rh = r % G;
+    const int qt = u % a.qtiles, kv = (u / a.qtiles) % a.hkv, b = u / a.qtiles / a.hkv, t = qt * a.tok_per_tile + rt;
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    if (rt < a.tok_per_tile && t < a.n_draft) {
+        const size_t off = ((static_cast<size_t>(b) * a.n_draft + t) * a.hq + kv * G + rh) * D;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const size_t at = off + 8 * (sub + LPV * k);
+            load4(a.q, at, a.q_dtype, *reinterpret_cast<float (*)[4]>(&v[8 * k]));
+            load4(a.q, at + 4, a.q_dtype, *reinterpret_cast<float (*)[4]>(&v[8 * k + 4]));
+        }
+    }
+    __syncwarp();
+    float scale = a.score_scale;
+    if (a.k_bits != 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[8 * k + e] = flip_sign(v[8 * k + e], sign_bit(a.signs, 8 * (sub + LPV * k) + e));
+        fwht_registers(v);
+        fwht_lanes<32, LPV>(v, sub);
+        scale *= rsqrtf(static_cast<float>(D));
+    }
+    __half* hi = reinterpret_cast<__half*>(a.prep + static_cast<size_t>(u) * (GEN_ROWS * 4) * KD) + static_cast<size_t>(r) * KD;
+    __half* lo = hi + static_cast<size_t>(GEN_ROWS) * KD;
+    auto limit = [](float y) { return fabsf(y) > mma::QLIMIT ? copysignf(mma::QLIMIT, y) : y; };  // (NaN stays)
+    if (blockIdx.y == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t hw[4], lw[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v0 = limit(v[8 * k + 2 * e] * scale), v1 = limit(v[8 * k + 2 * e + 1] * scale);
+                hw[e] = ptx::pack_half2(v0, v1);
+                const float2 h = mma::half2_float2(hw[e]);
+                lw[e] = ptx::pack_half2(v0 - h.x, v1 - h.y);
+            }
+            *reinterpret_cast<uint4*>(hi + 8 * (sub + LPV * k)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            *reinterpret_cast<uint4*>(lo + 8 * (sub + LPV * k)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        }
+    }
+    // a key's sketch channels hold +-gamma, its others centroids times
+    // key_scale (which score_scale takes out): the projections put it back
+    const float coef = m ? sqrtf(0.5f * 3.14159265358979f) / m * a.key_scale * scale : 0.f;
+    const int s0 = static_cast<int>(blockIdx.y) * PREP_SKETCH;
+#pragma unroll 2
+    for (int j = s0; j < min(m, s0 + PREP_SKETCH); ++j) {
+        const float4* srow = reinterpret_cast<const float4*>(a.sketch + static_cast<size_t>(j) * D);
+        float y = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 p = __ldg(srow + 2 * (sub + LPV * k)), q = __ldg(srow + 2 * (sub + LPV * k) + 1);
+            y = fmaf(p.x, v[8 * k], y);
+            y = fmaf(p.y, v[8 * k + 1], y);
+            y = fmaf(p.z, v[8 * k + 2], y);
+            y = fmaf(p.w, v[8 * k + 3], y);
+            y = fmaf(q.x, v[8 * k + 4], y);
+            y = fmaf(q.y, v[8 * k + 5], y);
+            y = fmaf(q.z, v[8 * k + 6], y);
+            y = fmaf(q.w, v[8 * k + 7], y);
+        }
+        y = limit(group_sum<LPV>(y) * coef);
+        if (sub == 0) {
+            const __half h = __float2half_rn(y);
+            hi[D + j] = h;
+            lo[D + j] = __float2half_rn(y - __half2float(h));
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(GEN_THREADS, D == 256 ? 2 : 3) tree_general_kernel(const __grid_constant__ Args a) {
+    constexpr int BK = GEN_BK<D>;
     extern __shared__ __align__(16) uint8_t gsm[];
     const int m = a.qjl_dims, KD = D + m, KS = gen_qk_stride(D, m), VS = D + 8;
     __half* qh = reinterpret_cast<__half*>(gsm);
@@ -55,10 +146,12 @@ __global__ void __launch_bounds__(GEN_THREADS) tree_general_kernel(const __grid_
     __half* ks = ql + GEN_ROWS * KS;
     __half* vs = ks + BK * KS;
     float* kn = reinterpret_cast<float*>(vs + BK * VS);
-    float* qscale = kn + BK;
-    float* cent = qscale + GEN_ROWS;  // key centroids (key_scale c), then value centroids (sqrt(d)/4 c)
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % LPV, grp = lane / LPV;
+    float* vnorm = kn + BK;
+    float* cent = vnorm + BK;  // key centroids (key_scale c), then value centroids (sqrt(d)/4 c)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid < 32) cent[tid] = tid < 16 ? a.kcent32[tid] : a.vcent32[tid - 16];
+    ptx::wait_prerequisites();
+    ptx::launch_dependents();
     const Unit x = unit_of<BK>(a, static_cast<int>(blockIdx.x));
     const int G = a.group, split = static_cast<int>(blockIdx.y);
     float* mine = a.parts + (static_cast<size_t>(blockIdx.x) * a.n_split + split) * (GEN_ROWS * (D + 2));
@@ -69,75 +162,15 @@ __global__ void __launch_bounds__(GEN_THREADS) tree_general_kernel(const __grid_
         if (tid < GEN_ROWS) mine[GEN_ROWS * D + tid] = -INFINITY;
         return;
     }
-    // ---- queries: rotated (turbo keys), the sketch's projections appended,
-    // scaled to a largest magnitude of 1, as fp16 hi + lo
-    for (int base = warp * VPW; base < GEN_ROWS; base += (GEN_THREADS / 32) * VPW) {
-        const int r = base + grp, t = r / G, g = r % G;
-        const bool in = t < x.ntok;
-        float v[32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (in) {
-                const size_t off = ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + t) * a.hq + x.kv * G + g) * D +
-                                   8 * (sub + LPV * k);
-                float (&lo)[4] = *reinterpret_cast<float (*)[4]>(&v[8 * k]);
-                float (&hi)[4] = *reinterpret_cast<float (*)[4]>(&v[8 * k + 4]);
-                load4(a.q, off, a.q_dtype, lo);
-                load4(a.q, off + 4, a.q_dtype, hi);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[8 * k + e] = 0.f;
-            }
-        }
-        if (a.k_bits != 8) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[8 * k + e] = flip_sign(v[8 * k + e], sign_bit(a.signs, 8 * (sub + LPV * k) + e));
-            fwht_registers(v);
-            fwht_lanes<32, LPV>(v, sub);
-            const float rs = rsqrtf(static_cast<float>(D));
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= rs;
-        }
-        float big = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) big = fmaxf(big, fabsf(v[i]));
-        // the sketch's projections, twice: for the row's scale, then stored
-        // with it.  A key channel is centroid x key_scale, a sketch channel
-        // +-gamma: the projections carry the scale instead.
-        const float coef = m ? sqrtf(0.5f * 3.14159265358979f) / m * a.key_scale : 0.f;
-        auto project = [&](int j) {
-            const float* row = a.sketch + static_cast<size_t>(j) * D;
-            float s = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s = fmaf(__ldg(row + 8 * (sub + LPV * k) + e), v[8 * k + e], s);
-            return group_sum<LPV>(s) * coef;
-        };
-        for (int j = 0; j < m; ++j) big = fmaxf(big, fabsf(project(j)));
-        big = group_max<LPV>(big);
-        const float inv = big > 0.f ? 1.f / big : 0.f;
-        auto put = [&](int c, float y) {
-            const __half h = __float2half_rn(y);
-            qh[r * KS + c] = h;
-            ql[r * KS + c] = __float2half_rn(y - __half2float(h));
-        };
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) put(8 * (sub + LPV * k) + e, v[8 * k + e] * inv);
-        for (int j = 0; j < m; ++j) {
-            const float s = project(j);
-            if (sub == 0) put(D + j, s * inv);
-        }
-        if (sub == 0) qscale[r] = big;
+    // ---- queries, prepared by tree_general_prep_kernel
+    {
+        const uint4* src = reinterpret_cast<const uint4*>(a.prep + static_cast<size_t>(blockIdx.x) * (GEN_ROWS * 4) * KD);
+        const int per_row = KD / 8;
+        for (int r = warp; r < 2 * GEN_ROWS; r += GEN_THREADS / 32)  // (rows of the first term, then of the second)
+            for (int c = lane; c < per_row; c += 32)
+                copy16_async(ptx::smem_addr(qh + r * KS + 8 * c), src + r * per_row + c);
     }
-    __syncthreads();
     const int r0 = warp * 16 + lane / 4, r1 = r0 + 8;  // the lane's two rows
-    const float rs0 = qscale[r0] * a.score_scale, rs1 = qscale[r1] * a.score_scale;
     const uint64_t mk0 = r0 / G < x.ntok ? row_mask(a, x, x.tok0 + r0 / G) : 0ull;
     const uint64_t mk1 = r1 / G < x.ntok ? row_mask(a, x, x.tok0 + r1 / G) : 0ull;
     float o[D / 8][4], m0 = NOTHING, m1 = NOTHING, l0 = 0.f, l1 = 0.f;
@@ -147,61 +180,109 @@ __global__ void __launch_bounds__(GEN_THREADS) tree_general_kernel(const __grid_
         for (int q = 0; q < 4; ++q) o[i][q] = 0.f;
     const int kbytes = a.k_bits == 8 ? D : D * a.k_bits / 8, vbytes = a.v_bits == 8 ? D : D * a.v_bits / 8;
 
+    // A tile's packed rows come through registers, a tile ahead: this thread
+    // takes channel group cg (8 channels) of keys ck + KPP i.
+    constexpr int CH = D / 8, KPP = GEN_THREADS / CH, N = BK / KPP;
+    const int cg = tid % CH, ck = tid / CH;
+    uint2 kraw[N], vraw[N];
+    uint16_t knraw = 0, vnraw = 0, graw[2] = {0, 0};
+    uint32_t zraw[2] = {0u, 0u};
+    const int zw = m / 32;  // sketch words of a key
+    auto raw8 = [&](const uint8_t* row, int bits) -> uint2 {
+        if (bits == 8) return __ldg(reinterpret_cast<const uint2*>(row) + cg);
+        if (bits == 4) return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row) + cg), 0u);
+        if (bits == 2) return make_uint2(__ldg(reinterpret_cast<const uint16_t*>(row) + cg), 0u);
+        // 24 bits from byte 3 cg, in one or two words of the row
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + ((3 * cg) >> 2);
+        return make_uint2(__ldg(w), (3 * cg) & 3 ? __ldg(w + (((3 * cg) & 3) > 1)) : 0u);
+    };
+    auto fetch = [&](int j) {
+        const int key0 = j * BK, nk = min(BK, x.kend - key0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int key = ck + KPP * i;
+            kraw[i] = vraw[i] = make_uint2(0u, 0u);
+            if (key < nk) {
+                const size_t row = cache_row(a, x.b, x.kv, key0 + key);
+                kraw[i] = raw8(a.k_codes + row * kbytes, a.k_bits);
+                vraw[i] = raw8(a.v_codes + row * vbytes, a.v_bits);
+            }
+        }
+        if (tid < BK) {
+            knraw = vnraw = 0;
+            if (tid < nk) {
+                const size_t row = cache_row(a, x.b, x.kv, key0 + tid);
+                knraw = a.k_norms[row];
+                vnraw = a.v_norms[row];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = tid + GEN_THREADS * i;
+            zraw[i] = 0u;
+            graw[i] = 0;
+            if (at < BK * zw && at / zw < nk) {
+                const size_t row = cache_row(a, x.b, x.kv, key0 + at / zw);
+                zraw[i] = reinterpret_cast<const uint32_t*>(a.k_qjl + row * (m / 8))[at % zw];
+                graw[i] = a.k_gamma[row];
+            }
+        }
+    };
+    // eight values of a packed group, as fp16 pairs
+    auto values = [&](uint2 raw, int bits, const float* ct, float n) -> uint4 {
+        float y[8];
+        if (bits == 8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                y[e] = n * static_cast<float>(static_cast<int8_t>(((e < 4 ? raw.x : raw.y) >> (8 * (e & 3))) & 0xffu));
+        } else {
+            const uint32_t codes = bits == 3 ? __funnelshift_r(raw.x, raw.y, 8 * ((3 * cg) & 3)) : raw.x;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = n * ct[(codes >> (bits * e)) & ((1u << bits) - 1u)];
+        }
+        return make_uint4(ptx::pack_half2(y[0], y[1]), ptx::pack_half2(y[2], y[3]), ptx::pack_half2(y[4], y[5]),
+                          ptx::pack_half2(y[6], y[7]));
+    };
+    fetch(j0);
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (the queries: the loop's first barrier shares them)
     for (int j = j0; j < j1; ++j) {
         const int key0 = j * BK, nk = min(BK, x.kend - key0);
         // ---- the tile to fp16: keys as centroids (norms multiply the fp32
-        // scores), values times their norms; slots past the end are zeros
-        for (int i = tid; i < 2 * BK * (D / 8); i += GEN_THREADS) {
-            const bool isv = i >= BK * (D / 8);
-            const int w = isv ? i - BK * (D / 8) : i, key = w / (D / 8), c = w % (D / 8);
-            const int bits = isv ? a.v_bits : a.k_bits, rb = isv ? vbytes : kbytes;
-            uint4 h = make_uint4(0u, 0u, 0u, 0u);
-            if (key < nk) {
-                const size_t row = cache_row(a, x.b, x.kv, key0 + key);
-                const uint8_t* src = (isv ? a.v_codes : a.k_codes) + row * rb;
-                // (a value row that is not finite is left out of V~, where a
-                // zero weight would turn it into NaN for rows that do not see
-                // it; its key's score is NaN instead, for those that do)
-                const float vn = half_bits_to_float(a.v_norms[row]);
-                const bool fine = fabsf(vn) < INFINITY;
-                const float n = isv ? (fine ? vn : 0.f) : 1.f;
-                float y[8];
-                if (bits == 8) {
-                    const uint2 b8 = *reinterpret_cast<const uint2*>(src + 8 * c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] = n * static_cast<float>(
-                                       static_cast<int8_t>(((e < 4 ? b8.x : b8.y) >> (8 * (e & 3))) & 0xffu));
-                } else {
-                    const uint32_t codes = stream_bits(reinterpret_cast<const uint32_t*>(src), rb / 4, 8 * bits * c, 8 * bits);
-                    const float* ct = cent + (isv ? 16 : 0);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = n * ct[(codes >> (bits * e)) & ((1u << bits) - 1u)];
-                }
-                h = make_uint4(ptx::pack_half2(y[0], y[1]), ptx::pack_half2(y[2], y[3]), ptx::pack_half2(y[4], y[5]),
-                               ptx::pack_half2(y[6], y[7]));
-                if (!isv && c == 0) kn[key] = fine ? half_bits_to_float(a.k_norms[row]) : NAN;
-            } else if (!isv && c == 0) {
-                kn[key] = 0.f;
-            }
-            *reinterpret_cast<uint4*>(isv ? vs + key * VS + 8 * c : ks + key * KS + 8 * c) = h;
+        // scores), values times their norms; slots past the end are zeros.
+        // (A value row that is not finite is left out of V~, where a zero
+        // weight would turn it into NaN for rows that do not see it; its key's
+        // score is NaN instead, for those that do.)
+        if (tid < BK) {
+            const float vn = half_bits_to_float(vnraw);
+            const bool fine = fabsf(vn) < INFINITY;
+            kn[tid] = fine ? half_bits_to_float(knraw) : NAN;
+            vnorm[tid] = fine ? vn : 0.f;
         }
-        for (int i = tid; i < BK * (m / 32); i += GEN_THREADS) {  // the sketch's channels: +-gamma
-            const int key = i / (m / 32), w = i % (m / 32);
-            uint32_t z = 0;
-            uint16_t gm = 0;
-            if (key < nk) {
-                const size_t row = cache_row(a, x.b, x.kv, key0 + key);
-                z = reinterpret_cast<const uint32_t*>(a.k_qjl + row * (m / 8))[w];
-                gm = a.k_gamma[row];
-            }
+        __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const uint32_t lo = gm ^ (((z >> e) & 1u) ? 0u : 0x8000u), hi = gm ^ (((z >> (e + 1)) & 1u) ? 0u : 0x8000u);
-                *reinterpret_cast<uint32_t*>(ks + key * KS + D + 32 * w + e) = lo | (hi << 16);
+        for (int i = 0; i < N; ++i) {
+            const int key = ck + KPP * i;
+            uint4 k8 = values(kraw[i], a.k_bits, cent, 1.f), v8 = values(vraw[i], a.v_bits, cent + 16, vnorm[key]);
+            if (key >= nk) k8 = v8 = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(ks + key * KS + 8 * cg) = k8;
+            *reinterpret_cast<uint4*>(vs + key * VS + 8 * cg) = v8;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // the sketch's channels: +-gamma
+            const int at = tid + GEN_THREADS * i;
+            if (at < BK * zw) {
+                uint32_t* dst = reinterpret_cast<uint32_t*>(ks + (at / zw) * KS + D + 32 * (at % zw));
+                const uint32_t gm = graw[i];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const uint32_t lo = gm ^ (((zraw[i] >> e) & 1u) ? 0u : 0x8000u);
+                    const uint32_t hi = gm ^ (((zraw[i] >> (e + 1)) & 1u) ? 0u : 0x8000u);
+                    dst[e / 2] = lo | (hi << 16);
+                }
             }
         }
         __syncthreads();
+        if (j + 1 < j1) fetch(j + 1);
         // ---- scores
         float s[BK / 8][4];
 #pragma unroll
@@ -232,8 +313,8 @@ __global__ void __launch_bounds__(GEN_THREADS) tree_general_kernel(const __grid_
             for (int e = 0; e < 2; ++e) {
                 const int key = 8 * n + 2 * (lane & 3) + e;
                 const float kk = kn[key];
-                s[n][e] = key < nk && ((v0 >> key) & 1u) ? s[n][e] * kk * rs0 : -INFINITY;
-                s[n][2 + e] = key < nk && ((v1 >> key) & 1u) ? s[n][2 + e] * kk * rs1 : -INFINITY;
+                s[n][e] = key < nk && ((v0 >> key) & 1u) ? s[n][e] * kk : -INFINITY;
+                s[n][2 + e] = key < nk && ((v1 >> key) & 1u) ? s[n][2 + e] * kk : -INFINITY;
                 t0 = fmaxf(t0, s[n][e]);
                 t1 = fmaxf(t1, s[n][2 + e]);
             }
@@ -299,21 +380,83 @@ __global__ void __launch_bounds__(GEN_THREADS) tree_general_kernel(const __grid_
     }
 }
 
-// One warp per query row: block (unit, 8 rows).
-constexpr int MERGE_THREADS = 256;
+// The general kernel's output: block (unit, 2 rows), four warps a row.  Each
+// of them adds every fourth piece (so a call's few rows still keep many loads
+// in flight), the first joins the four and applies the inverse rotation.
+constexpr int GM_ROWS = 2, GM_WARPS = 4, GM_THREADS = GM_ROWS * GM_WARPS * 32, GM_BATCH = 4;
 template <int D>
-__global__ void __launch_bounds__(MERGE_THREADS) tree_general_merge_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(GM_THREADS) tree_general_merge_kernel(const __grid_constant__ Args a) {
+    constexpr int N = D / 32;
+    __shared__ float sums[GM_ROWS][GM_WARPS][D];
+    __shared__ float total[GM_ROWS][GM_WARPS];
+    ptx::wait_prerequisites();
+    ptx::launch_dependents();
     const Unit x = unit_of<GEN_BK<D>>(a, static_cast<int>(blockIdx.x));
-    const int r = static_cast<int>(blockIdx.y) * (MERGE_THREADS / 32) + (static_cast<int>(threadIdx.x) >> 5);
-    const int G = a.group, t = r / G, g = r % G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mr = warp / GM_WARPS, part = warp % GM_WARPS;
+    const int r = static_cast<int>(blockIdx.y) * GM_ROWS + mr, G = a.group, t = r / G, g = r % G;
     // rows past the sequence's drafts are left as they are (all n_draft rows of a refused sequence are zeros)
     const int rows = x.bad ? min(a.tok_per_tile, a.n_draft - x.tok0) : x.ntok;
-    if (t >= rows) return;
+    const bool live = t < rows;
+    const int np = x.bad || !live ? 0 : a.n_split;
     const float* first = a.parts + static_cast<size_t>(blockIdx.x) * a.n_split * (GEN_ROWS * (D + 2));
-    const size_t dst = ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + t) * a.hq + x.kv * G + g) * D;
-    merge_row<D>(
-        a, [&](int j) { return first + static_cast<size_t>(j) * (GEN_ROWS * (D + 2)); }, x.bad ? 0 : a.n_split, GEN_ROWS,
-        r, dst);
+    auto piece = [&](int j) { return first + static_cast<size_t>(j) * (GEN_ROWS * (D + 2)); };
+    float M = -INFINITY;
+    for (int j = lane; j < np; j += 32) M = fmaxf(M, __ldcg(piece(j) + GEN_ROWS * D + r));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+    float L = 0.f, e[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = 0.f;
+    for (int j0 = part; j0 < np; j0 += GM_WARPS * GM_BATCH) {
+        float v[GM_BATCH][N], w[GM_BATCH];
+#pragma unroll
+        for (int k = 0; k < GM_BATCH; ++k) {
+            const int j = j0 + GM_WARPS * k;
+            w[k] = 0.f;
+            float m = -INFINITY;
+            if (j < np) m = __ldcg(piece(j) + GEN_ROWS * D + r);
+            if (m > -INFINITY) {  // (an empty piece's rows were never written: they are not read)
+                w[k] = ptx::ex2(m - M);
+                L = fmaf(__ldcg(piece(j) + GEN_ROWS * (D + 1) + r), w[k], L);
+            }
+            const float* p = piece(w[k] != 0.f ? j : 0) + r * D + lane * N;
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float2 y = w[k] != 0.f ? __ldcg(reinterpret_cast<const float2*>(p + i)) : make_float2(0.f, 0.f);
+                v[k][i] = y.x;
+                v[k][i + 1] = y.y;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < GM_BATCH; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) e[i] = fmaf(v[k][i], w[k], e[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[mr][part][lane * N + i] = e[i];
+    if (lane == 0) total[mr][part] = L;
+    __syncthreads();
+    if (part != 0 || !live) return;
+    L = 0.f;
+#pragma unroll
+    for (int k = 0; k < GM_WARPS; ++k) L += total[mr][k];
+    const float inv = L == 0.f ? 0.f : a.out_scale / L;  // (NaN stays NaN)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float y = 0.f;
+#pragma unroll
+        for (int k = 0; k < GM_WARPS; ++k) y += sums[mr][k][lane * N + i];
+        e[i] = y * inv;
+    }
+    if (a.v_bits != 8) {
+        fwht_registers(e);
+        fwht_lanes<N, 32>(e, lane);
+        const float rs = rsqrtf(static_cast<float>(D));
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = flip_sign(e[i] * rs, sign_bit(a.signs, lane * N + i));
+    }
+    store_row<N>(a.out, ((static_cast<size_t>(x.b) * a.n_draft + x.tok0 + t) * a.hq + x.kv * G + g) * D + lane * N, e,
+                 a.out_dtype);
 }
 
 // The queries of the tensor-memory kernel, once a call: rotated (turbo keys),
@@ -505,7 +648,8 @@ static Plan general_plan(const tq_params& p, int batch, int n_draft, int sms) {
     // about three blocks an SM (what shared memory lets reside), fewer when the units alone fill them
     long long n = (3ll * sms + pl.units - 1) / pl.units;
     pl.n_split = static_cast<int>(n < 1 ? 1 : n > 256 ? 256 : n);
-    pl.bytes = static_cast<size_t>(pl.units) * pl.n_split * GEN_ROWS * (p.head_dim + 2) * sizeof(float);
+    pl.prep_bytes = static_cast<size_t>(pl.units) * (GEN_ROWS * 4) * (p.head_dim + p.qjl_dims);
+    pl.bytes = pl.prep_bytes + static_cast<size_t>(pl.units) * pl.n_split * GEN_ROWS * (p.head_dim + 2) * sizeof(float);
     return pl;
 }
 
@@ -515,10 +659,16 @@ static cudaError_t launch_general(const Args& a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(tree_general_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    tree_general_kernel<D><<<dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(a.n_split)), GEN_THREADS, smem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    tree_general_merge_kernel<D><<<dim3(static_cast<unsigned>(a.units), GEN_ROWS / (MERGE_THREADS / 32)), MERGE_THREADS, 0, s>>>(a);
-    return cudaGetLastError();
+    constexpr int per_block = PREP_THREADS / 32 * (32 / (D / 32));
+    const long long prep = (static_cast<long long>(a.units) * GEN_ROWS + per_block - 1) / per_block;
+    e = mma::launch_dependent(tree_general_prep_kernel<D>, dim3(static_cast<unsigned>(prep), a.qjl_dims ? (a.qjl_dims + PREP_SKETCH - 1) / PREP_SKETCH : 1),
+                              dim3(PREP_THREADS), 0u, s, a);
+    if (e != cudaSuccess) return e;
+    e = mma::launch_dependent(tree_general_kernel<D>, dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(a.n_split)),
+                              dim3(GEN_THREADS), static_cast<uint32_t>(smem), s, a);
+    if (e != cudaSuccess) return e;
+    return mma::launch_dependent(tree_general_merge_kernel<D>, dim3(static_cast<unsigned>(a.units), GEN_ROWS / GM_ROWS),
+                                 dim3(GM_THREADS), 0u, s, a);
 }
 
 static cudaError_t launch_mma(const Args& a, const Plan& pl, cudaStream_t s) {
@@ -605,6 +755,7 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
         a.max_blocks = pm->max_blocks;
         a.block_size = pm->block_size;
         a.num_blocks = pm->num_blocks;
+        a.block_magic = UINT64_MAX / static_cast<uint32_t>(pm->block_size) + 1;  // (block_size is 16 or more)
     }
     a.q_dtype = q_dtype;
     a.out_dtype = out_dtype;

@@ -1,5 +1,5 @@
-// What the tree-attention kernels share: their arguments, the merge of
-// partial results, and the visibility rule.
+// What the tree-attention kernels share: their arguments, the visibility rule,
+// addresses and stores.
 //
 // Query row (t, g) of unit (sequence b, kv head) is draft t with head g of
 // the kv head's group.  It sees the L = base[b] slots before the tree, and
@@ -40,6 +40,7 @@ struct Args {
     uint8_t* prep;               // prepared queries (tensor-memory kernel)
     const int32_t* table;        // paged, or null
     int max_blocks, block_size, num_blocks;
+    uint64_t block_magic;        // ceil(2^64 / block_size): t / block_size is the high word of t times it
     int q_dtype, out_dtype, batch, hq, hkv, group, capacity, n_draft;
     int k_bits, v_bits, qjl_dims;  // 8 bits: an int8 side
     int staged_norms;              // rows of norms are 16-byte aligned every 8 slots
@@ -100,12 +101,13 @@ __device__ __forceinline__ uint64_t row_mask(const Args& a, const Unit& x, int t
 // the pool sets TQ_DEVERR_PAGE and block 0 is read in its place.
 __device__ __forceinline__ size_t cache_row(const Args& a, int b, int kv, int t) {
     if (!a.table) return (static_cast<size_t>(b) * a.hkv + kv) * a.capacity + t;
-    int blk = a.table[static_cast<size_t>(b) * a.max_blocks + t / a.block_size];
+    const int page = static_cast<int>(__umul64hi(static_cast<uint64_t>(t), a.block_magic));
+    int blk = a.table[static_cast<size_t>(b) * a.max_blocks + page];
     if (blk < 0 || blk >= a.num_blocks) {
         if (a.err) atomicOr(a.err, TQ_DEVERR_PAGE);
         blk = 0;
     }
-    return (static_cast<size_t>(blk) * a.hkv + kv) * a.block_size + t % a.block_size;
+    return (static_cast<size_t>(blk) * a.hkv + kv) * a.block_size + (t - page * a.block_size);
 }
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, int dtype) {
@@ -132,71 +134,6 @@ __device__ __forceinline__ void store_row(void* base, size_t off, const float (&
                                                       pack16(e[4], e[5], dtype), pack16(e[6], e[7], dtype));
         }
     }
-}
-
-// The output of one row from its partial results, by one warp (D / 32
-// channels a lane): piece j holds unnormalised O_j with the reference m_j
-// (log2 units) and the sum l_j;
-//   out = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j,  M = max_j m_j,
-// then the inverse rotation (turbo values).  piece(j) gives a piece's rows
-// [rows][D], then [rows] m, then [rows] l.  A row that saw nothing is zero.
-constexpr int MERGE_BATCH = 16;
-template <int D, typename Piece>
-__device__ __forceinline__ void merge_row(const Args& a, Piece piece, int np, int rows, int r, size_t dst) {
-    constexpr int N = D / 32;
-    const int lane = static_cast<int>(threadIdx.x) & 31;
-    float M = -INFINITY;
-    for (int j = lane; j < np; j += 32) M = fmaxf(M, __ldcg(piece(j) + rows * D + r));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-    float L = 0.f, e[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = 0.f;
-    for (int j0 = 0; j0 < np; j0 += 32) {
-        float w = 0.f;  // the weight of piece j0 + lane
-        if (j0 + lane < np) {
-            const float* sp = piece(j0 + lane);
-            const float mk = __ldcg(sp + rows * D + r);
-            if (mk > -INFINITY) {
-                w = ptx::ex2(mk - M);
-                L = fmaf(__ldcg(sp + rows * D + rows + r), w, L);
-            }
-        }
-        const int nj = min(32, np - j0);
-        for (int b = 0; b < nj; b += MERGE_BATCH) {
-            float v[MERGE_BATCH][N], wk[MERGE_BATCH];
-#pragma unroll
-            for (int k = 0; k < MERGE_BATCH; ++k) {
-                wk[k] = __shfl_sync(kFullMask, w, (b + k) & 31);
-                if (b + k >= nj) wk[k] = 0.f;
-                // (an empty piece's rows were never written: they are not read)
-                const float* p = piece(j0 + (wk[k] != 0.f ? b + k : 0)) + r * D + lane * N;
-#pragma unroll
-                for (int i = 0; i < N; i += 2) {
-                    const float2 y = wk[k] != 0.f ? __ldcg(reinterpret_cast<const float2*>(p + i)) : make_float2(0.f, 0.f);
-                    v[k][i] = y.x;
-                    v[k][i + 1] = y.y;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < MERGE_BATCH; ++k)
-#pragma unroll
-                for (int i = 0; i < N; ++i) e[i] = fmaf(v[k][i], wk[k], e[i]);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(kFullMask, L, o);
-    const float inv = L == 0.f ? 0.f : a.out_scale / L;  // (NaN stays NaN)
-#pragma unroll
-    for (int i = 0; i < N; ++i) e[i] *= inv;
-    if (a.v_bits != 8) {
-        fwht_registers(e);
-        fwht_lanes<N, 32>(e, lane);
-        const float rs = rsqrtf(static_cast<float>(D));
-#pragma unroll
-        for (int i = 0; i < N; ++i) e[i] = flip_sign(e[i] * rs, sign_bit(a.signs, lane * N + i));
-    }
-    store_row<N>(a.out, dst + lane * N, e, a.out_dtype);
 }
 
 }  // namespace tree
