@@ -224,21 +224,26 @@ tq_status validate_codebook(const tq_codebook* cb, int head_dim, int bits) {
     return TQ_OK;
 }
 
-tq_status validate_cache(const tq_params& p, const tq_cache* c) {
+tq_status validate_cache(const tq_params& p, const tq_cache* c, bool rows) {
+    auto aligned = [](const void* at, int bytes) { return reinterpret_cast<uintptr_t>(at) % bytes == 0; };
+    auto codes = [&](const void* at, int row) { return aligned(at, rows && row % 16 ? 8 : 16); };
+    const int norm = rows ? 2 : 16, sketch = rows ? 4 : 16;
     if (!c) return TQ_ERR_INVALID_ARG;
     if (c->batch < 1 || c->capacity < 1) return TQ_ERR_INVALID_ARG;
     if (!c->k_codes || !c->k_norms || !c->v_codes || !c->v_norms) return TQ_ERR_INVALID_ARG;
-    if (!aligned16(c->k_codes) || !aligned16(c->k_norms) || !aligned16(c->v_codes) || !aligned16(c->v_norms))
+    if (!codes(c->k_codes, vector_bytes(p.k_mode, p.k_bits, p.head_dim)) || !aligned(c->k_norms, norm) ||
+        !codes(c->v_codes, vector_bytes(p.v_mode, p.v_bits, p.head_dim)) || !aligned(c->v_norms, norm))
         return TQ_ERR_ALIGNMENT;
     if (p.qjl_dims > 0) {
         if (!c->k_qjl || !c->k_gamma || !c->qjl_matrix) return TQ_ERR_INVALID_ARG;
-        if (!aligned16(c->k_qjl) || !aligned16(c->k_gamma) || !aligned16(c->qjl_matrix)) return TQ_ERR_ALIGNMENT;
+        if (!aligned(c->k_qjl, sketch) || !aligned(c->k_gamma, norm) || !aligned16(c->qjl_matrix)) return TQ_ERR_ALIGNMENT;
     }
     return TQ_OK;
 }
 
-tq_status validate_pages(const tq_params& p, const tq_cache* pool, const tq_block_table* table, PageMap* pm) {
-    tq_status st = validate_cache(p, pool);
+tq_status validate_pages(const tq_params& p, const tq_cache* pool, const tq_block_table* table, PageMap* pm,
+                         bool rows) {
+    tq_status st = validate_cache(p, pool, rows);
     if (st != TQ_OK) return st;
     if (!table || !table->d_table || table->batch < 1 || table->max_blocks < 1) return TQ_ERR_INVALID_ARG;
     // blocks of whole 16-token tiles keep every per-block copy 16-byte sized

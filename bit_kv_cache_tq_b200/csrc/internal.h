@@ -47,9 +47,12 @@ struct PageMap {
 
 tq_status validate_params(const tq_params* p);
 tq_status validate_codebook(const tq_codebook* cb, int head_dim, int bits);
-tq_status validate_cache(const tq_params& p, const tq_cache* c);
+// rows: for calls that move whole rows, arrays aligned to the rows' units will do
+// (norms 2 bytes, sketches 4, codes 16, or 8 where a row is not whole 16s).
+tq_status validate_cache(const tq_params& p, const tq_cache* c, bool rows = false);
 // A pool and block table (block size a multiple of 16); fills *pm.
-tq_status validate_pages(const tq_params& p, const tq_cache* pool, const tq_block_table* table, PageMap* pm);
+tq_status validate_pages(const tq_params& p, const tq_cache* pool, const tq_block_table* table, PageMap* pm,
+                         bool rows = false);
 bool aligned16(const void* ptr);
 // Bytes of one stored vector: d*bits/8 (TURBO) or d (INT8).
 int vector_bytes(int mode, int bits, int head_dim);

@@ -64,9 +64,9 @@ __device__ __forceinline__ void store8(void* base, size_t off, const float* x) {
 // The product runs over bits 0, 1, 3, 4; s and j are butterflies; the result's
 // fragment gives lane t the channels 32 j + 8 t .. + 7, whole 16-byte stores.
 // Centroids are fp16 at the codebook's scale (2^-11 at most); fp32 outputs add
-// a second term with what the rounding left.  It moves 2.4 KB for 16 vectors
-// at 4 bits to bf16 and issues about 350 instructions a warp, against 800 with
-// the butterflies in lanes and shuffles.
+// a second term with what the rounding left.  (2 x 32768 tokens x 8 heads, K4
+// and V2 to bf16: 75 us, 4.2 TB/s; 132 us with all butterflies in lanes and
+// shuffles, bound by issue.)
 constexpr int THREADS = 256;
 
 template <int BITS, bool LO>
@@ -98,10 +98,10 @@ __device__ __forceinline__ void read_turbo(const Args& a, int side) {
         }
     }
     __syncthreads();
-    const int b = static_cast<int>(blockIdx.y);
+    const int b = static_cast<int>(blockIdx.x);
     const int start = a.starts[b], count = a.counts[b];
     if (start < 0 || count < 0 || count > a.max_count || start > a.capacity - count) {
-        if (a.err && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_POSITION);
+        if (a.err && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_POSITION);
         return;
     }
     const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2, copy = lane & (copies - 1);
@@ -128,17 +128,18 @@ __device__ __forceinline__ void read_turbo(const Args& a, int side) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) sg[j / 4] |= sign_bit(a.signs, 32 * j + 8 * t + e) << (8 * (j % 4) + e);
     const float factor = rsqrtf(static_cast<float>(D)) / a.scale[side];
-    const int runs = (count + 15) / 16, tiles = runs * a.hkv;
-    const int nwarps = gridDim.x * (THREADS / 32);
+    const int runs = count / 16 + (count % 16 != 0);
+    const long long tiles = static_cast<long long>(runs) * a.hkv;
+    const int nwarps = gridDim.y * (THREADS / 32);
     size_t h = 0;
     int t0 = 0;
     bool ok[2];
     uint16_t nraw[2];
     uint32_t lo[2][J], hi[2][BITS == 3 ? J : 1];  // the lane's codes of group j (3 bits: in two words)
-    auto fetch = [&](int w) {  // 16 tokens of one head
-        const int hw = w / runs;
+    auto fetch = [&](uint32_t w) {  // 16 tokens of one head
+        const uint32_t hw = w / static_cast<uint32_t>(runs);
         h = hw;
-        t0 = (w - hw * runs) * 16;
+        t0 = static_cast<int>(w - hw * runs) * 16;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int tok = t0 + g + 8 * r;
@@ -170,9 +171,8 @@ __device__ __forceinline__ void read_turbo(const Args& a, int side) {
             nraw[r] = s.norms[slot];
         }
     };
-    int w = blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
-    for (; w < tiles; w += nwarps) {
-        fetch(w);
+    for (long long w = static_cast<long long>(blockIdx.y) * (THREADS / 32) + threadIdx.x / 32; w < tiles; w += nwarps) {
+        fetch(static_cast<uint32_t>(w));
         float norm[2];
         bool live[2];
         uint32_t code[2][J];  // the 8 codes of group j, from bit 0
@@ -265,16 +265,16 @@ __device__ __forceinline__ void read_other(const Args& a, int side) {
     __shared__ float scen[16];
     if (threadIdx.x < 16) scen[threadIdx.x] = s.centroids[threadIdx.x];
     __syncthreads();
-    const int b = static_cast<int>(blockIdx.y);
+    const int b = static_cast<int>(blockIdx.x);
     const int start = a.starts[b], count = a.counts[b];
     if (start < 0 || count < 0 || count > a.max_count || start > a.capacity - count) {
-        if (a.err && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_POSITION);
+        if (a.err && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_POSITION);
         return;
     }
     const int lane = threadIdx.x & 31, sub = lane % LPV, grp = lane / LPV;
     const long long total = static_cast<long long>(count) * a.hkv;
-    const long long nwarps = static_cast<long long>(gridDim.x) * (blockDim.x / 32);
-    for (long long base = (static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32) * VPW;
+    const long long nwarps = static_cast<long long>(gridDim.y) * (blockDim.x / 32);
+    for (long long base = (static_cast<long long>(blockIdx.y) * (blockDim.x / 32) + threadIdx.x / 32) * VPW;
          base < total; base += nwarps * VPW) {
         const long long v = base + grp;
         bool valid = v < total;
@@ -345,7 +345,7 @@ __device__ __forceinline__ void read_other(const Args& a, int side) {
     }
 }
 
-// Grid: (blocks, batch, side).
+// Grid: (batch, blocks of a sequence, side).
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 2) read_back_kernel(const __grid_constant__ Args a) {
     const int side = static_cast<int>(blockIdx.z);
@@ -368,13 +368,14 @@ static cudaError_t launch_typed(Args& a, int sms, cudaStream_t s) {
                                                      : sizeof(Table<2, DTYPE == 0>));
         if (n > bytes) bytes = n;
     }
-    const cudaError_t e =
-        cudaFuncSetAttribute(read_back_kernel<D, DTYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // (the largest table's for every call: another thread's call may set it between this line and the launch)
+    const cudaError_t e = cudaFuncSetAttribute(read_back_kernel<D, DTYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sizeof(Table<4, DTYPE == 0>)));
     if (e != cudaSuccess) return e;
     // eight warps a block and 16 vectors a warp, two blocks an SM and side, shared by the sequences
-    const long long want = (static_cast<long long>((a.max_count + 15) / 16) * a.hkv + 7) / 8;
+    const long long want = ((a.max_count / 16 + 1ll) * a.hkv + 7) / 8;
     const long long most = (2ll * sms + a.batch - 1) / a.batch;
-    const dim3 grid(static_cast<unsigned>(want < most ? want : most), static_cast<unsigned>(a.batch), 2);
+    const dim3 grid(static_cast<unsigned>(a.batch), static_cast<unsigned>(want < most ? want : most), 2);
     a.copies_log2 = want <= most ? 2 : 5;
     read_back_kernel<D, DTYPE><<<grid, THREADS, bytes, s>>>(a);
     return cudaGetLastError();
@@ -437,7 +438,6 @@ static tq_status read(const tq_params* params, const tq_codebook* kcb, const tq_
         a.block_size = pm->block_size;
         a.num_blocks = pm->num_blocks;
     }
-    if (a.batch > 65535) return TQ_ERR_INVALID_ARG;
     rotation_sign_bits(p.seed, p.head_dim, a.signs);
     const int sms = num_sms_current();
     if (sms <= 0) return TQ_ERR_CUDA;

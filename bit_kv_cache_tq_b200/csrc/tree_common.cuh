@@ -78,7 +78,7 @@ __device__ __forceinline__ Unit unit_of(const Args& a, int u) {
     x.bad = x.drafts < 0 || x.drafts > a.n_draft || x.base < 0 || x.base > a.capacity - x.drafts;
     x.ntok = x.bad ? 0 : max(0, min(a.tok_per_tile, x.drafts - x.tok0));
     x.kend = x.ntok > 0 ? x.base + x.drafts : 0;
-    x.ntiles = (x.kend + BK - 1) / BK;
+    x.ntiles = static_cast<int>((static_cast<uint32_t>(x.kend) + BK - 1) / BK);
     return x;
 }
 

@@ -433,15 +433,26 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_for(t, stream):
-    """The stream's handle; t is one of the call's tensors, which lie on the current device."""
-    if stream is not None:
-        return stream.cuda_stream
-    device = t.get_device()
-    if device != torch.cuda.current_device():
-        raise ValueError("the tensors are on device %d, the current device is %d"
-                         % (device, torch.cuda.current_device()))
-    return _raw_stream(device) if _raw_stream else torch.cuda.current_stream().cuda_stream
+def _code(t):
+    try:
+        return _CODES[t.dtype]
+    except KeyError:
+        raise ValueError("fp32, bf16 or fp16 is wanted, not %s" % t.dtype) from None
+
+
+def _stream_for(stream, *tensors):
+    """The handle of the stream (None: torch's current one); the call's tensors lie on the current device, as does it."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("the call's tensors are on more than one device")
+    if device < 0 or device != torch.cuda.current_device():
+        raise ValueError("the call's tensors are not on the current CUDA device")
+    if stream is None:
+        return _raw_stream(device) if _raw_stream else torch.cuda.current_stream().cuda_stream
+    if stream.device_index != device:
+        raise ValueError("the stream is of another device than the call's tensors")
+    return stream.cuda_stream
 
 
 def _cache_ref(cache):
@@ -499,7 +510,7 @@ def _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, batch,
     if rope_positions is not None:
         _check_int32(rope_positions, batch * shape[1], "rope_positions")
     return (ctypes.byref(params), _ref(kcb), _ref(vcb), ctypes.byref(rope), _address(q), stride, k_new.data_ptr(),
-            _token_stride(k_new, "k_new"), v_new.data_ptr(), _token_stride(v_new, "v_new"), _CODES[k_new.dtype],
+            _token_stride(k_new, "k_new"), v_new.data_ptr(), _token_stride(v_new, "v_new"), _code(k_new),
             shape[1], positions.data_ptr(), _address(rope_positions), _cache_ref(cache))
 
 
@@ -509,7 +520,8 @@ def tq_rope_append(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, q_
     positions[b] ..; rope_positions: int32 [batch, n_new] or None (the slots).  q, k_new and v_new may be slices of one
     projection's output; q and q_out may be None, or the same contiguous tensor."""
     args = _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, cache, cache.batch, q_out, rope_positions)
-    _check(_lib.tq_rope_append(*args, _address(q_out), _address(error), _stream_for(k_new, stream)), "tq_rope_append")
+    handle = _stream_for(stream, k_new, v_new, q, q_out, positions, rope_positions, cache.k_codes, error)
+    _check(_lib.tq_rope_append(*args, _address(q_out), _address(error), handle), "tq_rope_append")
 
 
 def tq_rope_append_paged(params, kcb, vcb, rope, q, k_new, v_new, positions, pool, table, q_out, rope_positions=None,
@@ -517,8 +529,9 @@ def tq_rope_append_paged(params, kcb, vcb, rope, q, k_new, v_new, positions, poo
     """tq_rope_append on a paged cache (see tq_quantize_append_paged)."""
     bt = block_table(table)
     args = _rope_call(params, kcb, vcb, rope, q, k_new, v_new, positions, pool, bt.batch, q_out, rope_positions)
-    _check(_lib.tq_rope_append_paged(*args, ctypes.byref(bt), _address(q_out), _address(error),
-                                     _stream_for(k_new, stream)), "tq_rope_append_paged")
+    handle = _stream_for(stream, k_new, v_new, q, q_out, positions, rope_positions, pool.k_codes, table, error)
+    _check(_lib.tq_rope_append_paged(*args, ctypes.byref(bt), _address(q_out), _address(error), handle),
+           "tq_rope_append_paged")
 
 
 def tq_tree_workspace_bytes(params, batch, n_draft):
@@ -528,20 +541,22 @@ def tq_tree_workspace_bytes(params, batch, n_draft):
     return int(n.value)
 
 
-def _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, cache, batch, out):
+def _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, cache, batch, out, workspace):
     shape = q.shape
     if len(shape) != 4 or shape[0] != batch or shape[2] != params.num_q_heads or shape[3] != params.head_dim or (
             not q.is_contiguous()):
         raise ValueError("q: a contiguous [batch, n_draft, num_q_heads, head_dim] is wanted")
     if out.shape != shape or not out.is_contiguous():
         raise ValueError("out: a contiguous tensor of q's shape is wanted")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor is wanted")
     if not (tree_mask.dtype is torch.int64 and tree_mask.is_cuda and tree_mask.is_contiguous()
             and tree_mask.shape == shape[:2]):
         raise ValueError("tree_mask: a contiguous int64 CUDA tensor [batch, n_draft] is wanted")
     _check_int32(base_lens, batch, "base_lens")
     if draft_lens is not None:
         _check_int32(draft_lens, batch, "draft_lens")
-    return (ctypes.byref(params), _ref(kcb), _ref(vcb), q.data_ptr(), _CODES[q.dtype], shape[1], tree_mask.data_ptr(),
+    return (ctypes.byref(params), _ref(kcb), _ref(vcb), q.data_ptr(), _code(q), shape[1], tree_mask.data_ptr(),
             base_lens.data_ptr(), _address(draft_lens), _cache_ref(cache))
 
 
@@ -550,19 +565,20 @@ def tq_tree_attention(params, kcb, vcb, q, tree_mask, base_lens, cache, out, wor
     """Attention of drafted tokens: q [batch, n_draft, Hq, d] over the base_lens[b] slots before the tree and, of the
     drafts in the slots after them, those whose bits tree_mask (int64 [batch, n_draft]) has set; out: like q, in fp32,
     bf16 or fp16.  workspace: uint8, tq_tree_workspace_bytes(params, batch, n_draft), any contents."""
-    args = _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, cache, cache.batch, out)
-    _check(_lib.tq_tree_attention(*args, out.data_ptr(), _CODES[out.dtype], workspace.data_ptr(), workspace.nbytes,
-                                  _address(error), _stream_for(q, stream)), "tq_tree_attention")
+    args = _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, cache, cache.batch, out, workspace)
+    handle = _stream_for(stream, q, out, tree_mask, base_lens, draft_lens, cache.k_codes, workspace, error)
+    _check(_lib.tq_tree_attention(*args, out.data_ptr(), _code(out), workspace.data_ptr(), workspace.nbytes,
+                                  _address(error), handle), "tq_tree_attention")
 
 
 def tq_tree_attention_paged(params, kcb, vcb, q, tree_mask, base_lens, pool, table, out, workspace, draft_lens=None,
                             error=None, stream=None):
     """tq_tree_attention on a paged cache (see tq_quantize_append_paged)."""
     bt = block_table(table)
-    args = _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, pool, bt.batch, out)
-    _check(_lib.tq_tree_attention_paged(*args, ctypes.byref(bt), out.data_ptr(), _CODES[out.dtype],
-                                        workspace.data_ptr(), workspace.nbytes, _address(error),
-                                        _stream_for(q, stream)), "tq_tree_attention_paged")
+    args = _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, pool, bt.batch, out, workspace)
+    handle = _stream_for(stream, q, out, tree_mask, base_lens, draft_lens, pool.k_codes, table, workspace, error)
+    _check(_lib.tq_tree_attention_paged(*args, ctypes.byref(bt), out.data_ptr(), _code(out), workspace.data_ptr(),
+                                        workspace.nbytes, _address(error), handle), "tq_tree_attention_paged")
 
 
 class draft_layers:
@@ -570,6 +586,8 @@ class draft_layers:
 
     def __init__(self, layers):
         self.layers = list(layers)
+        if not self.layers:
+            raise ValueError("at least one layer is wanted")
         self.tensors = [list(vars(c).values()) for _, c in self.layers]  # (whose addresses the structs hold)
         n = len(self.layers)
         self.params = (tq_params * n)(*[p for p, _ in self.layers])
@@ -591,20 +609,24 @@ def tq_commit_drafts(layers, path, path_lens, base_lens, new_lens=None, error=No
     """Move draft path[b, i] (int32 [batch, max_path]) to slot base_lens[b] + i, i < path_lens[b], in every layer of a
     draft_layers; new_lens: base_lens + path_lens."""
     args = _commit_call(path, path_lens, base_lens, new_lens, layers.caches[0].batch)
-    _check(_lib.tq_commit_drafts(len(layers.layers), layers.params, layers.caches, *args, _address(error),
-                                 _stream_for(path, stream)), "tq_commit_drafts")
+    handle = _stream_for(stream, path, path_lens, base_lens, new_lens, layers.layers[0][1].k_codes, error)
+    _check(_lib.tq_commit_drafts(len(layers.layers), layers.params, layers.caches, *args, _address(error), handle),
+           "tq_commit_drafts")
 
 
 def tq_commit_drafts_paged(layers, table, path, path_lens, base_lens, new_lens=None, error=None, stream=None):
     """tq_commit_drafts on paged caches that share one block table."""
     bt = block_table(table)
     args = _commit_call(path, path_lens, base_lens, new_lens, bt.batch)
+    handle = _stream_for(stream, path, path_lens, base_lens, new_lens, layers.layers[0][1].k_codes, table, error)
     _check(_lib.tq_commit_drafts_paged(len(layers.layers), layers.params, layers.caches, ctypes.byref(bt), *args,
-                                       _address(error), _stream_for(path, stream)), "tq_commit_drafts_paged")
+                                       _address(error), handle), "tq_commit_drafts_paged")
 
 
 def _read_call(params, starts, counts, batch, k_out, v_out):
     out = v_out if k_out is None else k_out
+    if out is None:
+        raise ValueError("k_out or v_out is wanted")
     shape = out.shape
     if len(shape) != 4 or shape[0] != batch or shape[2] != params.num_kv_heads or shape[3] != params.head_dim or (
             not out.is_contiguous()):
@@ -614,15 +636,16 @@ def _read_call(params, starts, counts, batch, k_out, v_out):
         raise ValueError("k_out and v_out must be alike")
     _check_int32(starts, batch, "starts")
     _check_int32(counts, batch, "counts")
-    return starts.data_ptr(), counts.data_ptr(), shape[1], _CODES[out.dtype], _address(k_out), _address(v_out)
+    return starts.data_ptr(), counts.data_ptr(), shape[1], _code(out), _address(k_out), _address(v_out)
 
 
 def tq_read_back(params, kcb, vcb, cache, starts, counts, k_out=None, v_out=None, error=None, stream=None):
     """Reconstruct slots starts[b] .. starts[b] + counts[b] - 1 of every sequence into k_out and v_out
     ([batch, max_count, Hkv, d], fp32, bf16 or fp16); rows past counts[b] are left as they are."""
     args = _read_call(params, starts, counts, cache.batch, k_out, v_out)
+    handle = _stream_for(stream, starts, counts, k_out, v_out, cache.k_codes, error)
     _check(_lib.tq_read_back(ctypes.byref(params), _ref(kcb), _ref(vcb), _cache_ref(cache), *args, _address(error),
-                             _stream_for(starts, stream)), "tq_read_back")
+                             handle), "tq_read_back")
 
 
 def tq_read_back_paged(params, kcb, vcb, pool, table, starts, counts, k_out=None, v_out=None, error=None,
@@ -630,8 +653,9 @@ def tq_read_back_paged(params, kcb, vcb, pool, table, starts, counts, k_out=None
     """tq_read_back on a paged cache (see tq_quantize_append_paged)."""
     bt = block_table(table)
     args = _read_call(params, starts, counts, bt.batch, k_out, v_out)
+    handle = _stream_for(stream, starts, counts, k_out, v_out, pool.k_codes, table, error)
     _check(_lib.tq_read_back_paged(ctypes.byref(params), _ref(kcb), _ref(vcb), _cache_ref(pool), ctypes.byref(bt),
-                                   *args, _address(error), _stream_for(starts, stream)), "tq_read_back_paged")
+                                   *args, _address(error), handle), "tq_read_back_paged")
 
 
 def tq_read_device_error(error, stream=None, timeout_ms=2000):

@@ -571,8 +571,8 @@ tq_status tq_rope_append_paged(const tq_params* params, const tq_codebook* kcb, 
  * slots would.  A draft that sees nothing gets zeros.
  *   d_q           device, [batch][n_draft][Hq][d] in q_dtype.
  *   n_draft       1 .. 64 (more: TQ_ERR_UNSUPPORTED).
- *   d_mask        device uint64 [batch][n_draft]; bits at or past the
- *                 sequence's draft count are ignored.
+ *   d_mask        device uint64 [batch][n_draft], 8-byte aligned; bits at or
+ *                 past the sequence's draft count are ignored.
  *   d_base_lens   device int32 [batch], 0 or more.
  *   d_draft_lens  device int32 [batch], drafts of each sequence (0 .. n_draft),
  *                 or NULL: n_draft for all.  Output rows of a sequence past
@@ -586,7 +586,10 @@ tq_status tq_rope_append_paged(const tq_params* params, const tq_codebook* kcb, 
  * entry outside the pool sets TQ_DEVERR_PAGE; that sequence's output is not
  * valid.  sparse_v_threshold is not applied.  Every configuration of
  * tq_params is taken; outputs are within 2e-3 (relative L2 per row) of exact
- * attention over the stored codes, plus the rounding to out_dtype.
+ * attention over the stored codes, plus the rounding to out_dtype.  (bf16
+ * outputs of d = 128 layers without a sketch take their queries in 11 bits, the
+ * others in about 22.)  TQ_ERR_UNSUPPORTED also where the device reserves
+ * another amount of shared memory per block than 1 KB (d = 128 without a sketch).
  */
 tq_status tq_tree_attention(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const void* d_q,
                             tq_dtype q_dtype, int32_t n_draft, const uint64_t* d_mask, const int32_t* d_base_lens,
@@ -607,7 +610,10 @@ tq_status tq_tree_workspace_bytes(const tq_params* params, int32_t batch, int32_
  * what they held.
  *   n_layers      layers; params and caches are host arrays of that length.
  *                 The layers may differ in heads, widths and modes, not in
- *                 batch or capacity.
+ *                 batch or capacity.  Arrays may be aligned to their rows'
+ *                 units only (norms 2 bytes, sketches 4, codes 16, or 8 where a
+ *                 row is not whole 16s), as those of layers that lie in one
+ *                 allocation are.
  *   d_path        device int32 [batch][max_path], draft indices 0 .. 63.
  *   max_path      1 .. 64.
  *   d_path_lens   device int32 [batch], 0 .. max_path.

@@ -244,3 +244,41 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     for outs in ((k, k), (k, k.half()), (q, None), (None, k[:1])):
         with pytest.raises(ValueError):
             tq.tq_read_back(p, kcb, vcb, cache, i32, i32, *outs)
+
+
+def test_more_refusals_of_values_and_places():
+    """Values that leave the kernels' range, addresses they could not load, and calls without anything to do."""
+    for kw in (dict(scaling=tq.TQ_ROPE_SCALE_LINEAR, factor=5e-324),
+               dict(scaling=tq.TQ_ROPE_SCALE_WAVELENGTH, factor=5e-324, trained_len=2.0)):
+        with pytest.raises(tq.TqError) as e:  # a frequency past the doubles
+            tq.tq_rope_init(64, **kw)
+        assert e.value.status == tq.TQ_ERR_INVALID_ARG
+    for paged in (False, True):
+        for magnitude in (1e300, 1e-300):  # infinity and zero in fp32
+            assert _rope_status(paged, magnitude=magnitude) == tq.TQ_ERR_INVALID_ARG
+        assert _tree_status(paged, mask=AT + 4) == tq.TQ_ERR_ALIGNMENT
+    p, kcb, vcb, cache, i32 = _cpu_call()
+    with pytest.raises(ValueError):
+        tq.draft_layers([])
+    with pytest.raises(ValueError):
+        tq.tq_read_back(p, kcb, vcb, cache, i32, i32)
+
+
+def test_commit_takes_rows_at_their_own_alignment():
+    """Norms need 2 bytes, codes of whole 16-byte rows 16, of 24-byte rows 8 (the calls that load them otherwise: 16).
+    An index that no layer can hold ends the accepted calls before anything is launched."""
+    for name, at, status in (("k_norms", AT + 2, tq.TQ_OK), ("v_norms", AT + 6, tq.TQ_OK),
+                             ("k_norms", AT + 1, tq.TQ_ERR_ALIGNMENT), ("v_codes", AT + 8, tq.TQ_ERR_ALIGNMENT)):
+        def change(params, caches, name=name, at=at):
+            setattr(caches[0], name, at)
+            caches[1].batch = 0 if status == tq.TQ_OK else 3  # (the second layer is refused for its batch)
+        assert _commit_status(change=change) == (tq.TQ_ERR_INVALID_ARG if status == tq.TQ_OK else status)
+
+    def narrow(off):
+        def change(params, caches):
+            params[0] = params[1] = tq.make_params(64, 8, 2, 3, 3)
+            caches[0].k_codes = AT + off
+            caches[1].batch = 0
+        return change
+    assert _commit_status(change=narrow(8)) == tq.TQ_ERR_INVALID_ARG
+    assert _commit_status(change=narrow(4)) == tq.TQ_ERR_ALIGNMENT

@@ -667,3 +667,158 @@ def test_two_trees_at_once():
             tq.tq_tree_attention(layer.params, layer.kcb, layer.vcb, q, mask, base, cache, o, w, error=err, stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_tree_many_short_units_in_one_block():
+    """Blocks that walk a dozen units of one tile each, of which one of the two streams has none."""
+    layer = _layer(128, 32, 32, 4, 2)
+    batch, n = 60, 5
+    cache, _ = R.make_cache(layer, batch, 64)
+    R.fill(layer, cache, None, batch, 64, seed=4)
+    bases = [b % 60 for b in range(batch)]
+    mask = R.random_tree(batch, n, seed=6)
+    q = torch.randn(batch, n, 32, 128, generator=torch.Generator().manual_seed(7))
+    for dtype in (BF16, FP32):
+        qd = q.to(dtype)
+        outs = []
+        for _ in range(5):
+            out = torch.empty_like(qd, device="cuda")
+            _tree_call(layer, qd.cuda(), torch.from_numpy(mask).cuda(), bases, cache, None, out)
+            outs.append(out)
+        assert all(torch.equal(o, outs[0]) for o in outs)
+        for b in (0, 7, 31, 59):
+            class One:
+                batch, capacity = 1, 64
+            one = One()
+            for name in ("k_codes", "k_norms", "v_codes", "v_norms"):
+                setattr(one, name, getattr(cache, name)[b:b + 1])
+            want = R.tree_attention(layer, one, qd[b:b + 1].double().numpy(), mask[b:b + 1], bases[b:b + 1], [n])
+            _check_rows(outs[0][b:b + 1], want, dtype)
+
+
+@pytest.mark.parametrize("kb,qjl", [(4, 0), (8, 0), (3, 32)])
+def test_read_back_of_many_sequences(kb, qjl):
+    """More sequences than a grid's second dimension holds: the last ones give what a short batch gives."""
+    layer = _layer(64, 1, 1, kb, 2, qjl)
+    batch, slots, n = 66000, 16, 2
+    cache, _ = R.make_cache(layer, batch, slots)
+    few, _ = R.make_cache(layer, 3, slots)
+    R.fill(layer, few, None, 3, slots, seed=3)
+    for name in _names(cache):
+        getattr(cache, name)[-3:] = getattr(few, name)
+    starts, counts = _ints([0] * (batch - 3) + [1, 0, 14]), _ints([0] * (batch - 3) + [2, 1, 2])
+    out = [torch.full((batch, n, 1, 64), 7.0, dtype=BF16, device="cuda") for _ in "kv"]
+    want = [torch.full((3, n, 1, 64), 7.0, dtype=BF16, device="cuda") for _ in "kv"]
+    err = _err()
+    tq.tq_read_back(layer.params, layer.kcb, layer.vcb, cache, starts, counts, *out, error=err)
+    tq.tq_read_back(layer.params, layer.kcb, layer.vcb, few, starts[-3:].clone(), counts[-3:].clone(), *want, error=err)
+    assert tq.tq_read_device_error(err) == (tq.TQ_OK, 0)
+    for o, w in zip(out, want):
+        assert torch.equal(o[-3:], w) and torch.all(o[:-3] == 7.0)
+
+
+def test_calls_from_two_threads():
+    """Two host threads with layers of different widths, a stream each: no call depends on the other's launch state."""
+    import threading
+    work = []
+    for d, qjl, kb in ((256, 0, 4), (256, 256, 4), (128, 32, 3), (128, 128, 3)):
+        layer = _layer(d, 4, 2, kb, 2, qjl)
+        cache, _ = R.make_cache(layer, 1, 300)
+        R.fill(layer, cache, None, 1, 300, seed=d + qjl)
+        q = torch.randn(1, 4, 4, d, generator=torch.Generator().manual_seed(qjl)).to(BF16).cuda()
+        mask, base = torch.from_numpy(R.random_tree(1, 4, seed=2)).cuda(), _ints([280])
+        ws = torch.empty(tq.tq_tree_workspace_bytes(layer.params, 1, 4), dtype=torch.uint8, device="cuda")
+        out, back = torch.empty_like(q), torch.empty(1, 300, 2, d, device="cuda")
+        work.append((layer, cache, q, mask, base, ws, out, back, _ints([0]), _ints([300])))
+
+    def call(w, stream=None):
+        layer, cache, q, mask, base, ws, out, back, start, count = w
+        tq.tq_tree_attention(layer.params, layer.kcb, layer.vcb, q, mask, base, cache, out, ws, stream=stream)
+        tq.tq_read_back(layer.params, layer.kcb, layer.vcb, cache, start, count, None, back, stream=stream)
+
+    for w in work:
+        call(w)
+    torch.cuda.synchronize()
+    want = [(w[6].clone(), w[7].clone()) for w in work]
+    failed = []
+
+    def run(w):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(100):
+                call(w, stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001 - reported below
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(w,)) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    assert all(torch.equal(w[6], a) and torch.equal(w[7], b) for w, (a, b) in zip(work, want))
+
+
+def test_binding_refuses_places_and_types():
+    """Host tensors beside device ones, types without a code, a workspace with gaps: refused before the library."""
+    layer = _layer(128, 4, 2, 4, 2)
+    cache, _ = R.make_cache(layer, 1, 64)
+    rope, pos = tq.tq_rope_init(128), _ints([0])
+    q, k = torch.zeros(1, 1, 4, 128, device="cuda"), torch.zeros(1, 1, 2, 128, device="cuda")
+    mask = torch.ones(1, 1, dtype=torch.int64, device="cuda")
+    ws = torch.empty(tq.tq_tree_workspace_bytes(layer.params, 1, 1), dtype=torch.uint8, device="cuda")
+    a = (layer.params, layer.kcb, layer.vcb)
+    for stream in (None, torch.cuda.Stream()):
+        for args in ((q.cpu(), k, k, pos, cache, q), (q, k.cpu(), k, pos, cache, q), (q, k, k, pos, cache, q.cpu()),
+                     (q.double(), k.double(), k.double(), pos, cache, q.double())):
+            with pytest.raises(ValueError):
+                tq.tq_rope_append(*a, rope, *args, stream=stream)
+        for args in ((q.cpu(), mask, pos, cache, q, ws), (q, mask, pos, cache, q.cpu(), ws),
+                     (q, mask, pos, cache, q, ws.cpu()), (q, mask, pos, cache, q, ws[::2]),
+                     (q, mask, pos, cache, q.double(), ws)):
+            with pytest.raises(ValueError):
+                tq.tq_tree_attention(*a, *args, stream=stream)
+        for out in (k.cpu(), k.double()):
+            with pytest.raises(ValueError):
+                tq.tq_read_back(*a, cache, pos, pos, out, stream=stream)
+
+
+@pytest.mark.parametrize("d,kb,vb,qjl", [(128, 4, 2, 0), (64, 3, 2, 32), (64, 3, 8, 0), (128, 8, 3, 0)])
+def test_commit_of_layers_in_one_allocation(d, kb, vb, qjl):
+    """Layers that lie in one allocation at their own sizes, so that all but the first are aligned to their rows only."""
+    layers, batch, hkv, capacity, n = 3, 3, 1, 37, 9
+    layer = _layer(d, hkv, hkv, kb, vb, qjl)
+    g = torch.Generator().manual_seed(d + kb)
+    rows = batch * hkv * capacity
+
+    def stack(per_row, dtype=torch.uint8):
+        a = torch.randint(0, 256, (layers * rows * per_row,), generator=g, dtype=torch.uint8).cuda()
+        shape = (layers, batch, hkv, capacity) + (() if dtype is torch.int16 else (per_row,))
+        return a.view(dtype).view(shape)
+
+    one = tq.alloc_cache(layer.params, 1, 16)
+    a = {"k_codes": stack(one.k_codes.shape[-1]), "v_codes": stack(one.v_codes.shape[-1]),
+         "k_norms": stack(2, torch.int16), "v_norms": stack(2, torch.int16)}
+    if qjl:
+        a["k_qjl"], a["k_gamma"] = stack(qjl // 8), stack(2, torch.int16)
+    before = {m: t.clone() for m, t in a.items()}
+    caches = [tq.CacheTensors(batch, capacity, a["k_codes"][i], a["k_norms"][i], a["k_qjl"][i] if qjl else None,
+                              a["k_gamma"][i] if qjl else None, a["v_codes"][i], a["v_norms"][i], one.qjl_matrix)
+              for i in range(layers)]
+    assert caches[1].k_norms.data_ptr() % 16
+    base, paths = [0, 11, 28], [[1, 4, 8], [], [0, 2, 3, 5, 6, 7]]
+    path = torch.zeros(batch, n, dtype=torch.int32)
+    for b, p in enumerate(paths):
+        path[b, : len(p)] = torch.tensor(p, dtype=torch.int32)
+    new, err = _ints([0] * batch), _err()
+    tq.tq_commit_drafts(tq.draft_layers([(layer.params, c) for c in caches]), path.cuda(),
+                        _ints([len(p) for p in paths]), _ints(base), new, err)
+    assert tq.tq_read_device_error(err) == (tq.TQ_OK, 0)
+    for m, t in a.items():
+        want = before[m].clone()
+        for b, p in enumerate(paths):
+            for i, x in enumerate(p):
+                want[:, b, :, base[b] + i] = before[m][:, b, :, base[b] + x]
+        assert torch.equal(t, want), m
+    assert new.tolist() == [base[b] + len(p) for b, p in enumerate(paths)]
