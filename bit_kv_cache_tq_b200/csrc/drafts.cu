@@ -18,7 +18,7 @@ constexpr int MAX_PATH = 64;
 constexpr int LAYERS_PER_LAUNCH = 64;
 constexpr int THREADS = 256;
 
-constexpr int HEADS = 4;  // kv heads of one block
+constexpr int HEADS = 2;  // kv heads of one block
 
 struct Layer {
     uint8_t* k_codes;
@@ -100,16 +100,17 @@ __device__ __forceinline__ void move_codes(const Layer& y, const long long* from
     v.store(vc, from, to, n, heads, head);
 }
 
-// Block (sequence and group of heads, layer).  It is latency: a chain of
-// length, path, row and write; several heads a block share the chain's start
-// and keep more rows in flight.  (48 sequences x 32 layers x 8 heads, up to 64
-// rows of 116 bytes each: 67 us with a block per head and divisions in the
-// row index, 31 us in this form, 2.9 TB/s; a norm's 2 bytes cost a sector of 32
-// each way.)
-// SMALL: every layer's rows are of at most 64 bytes, in 16-byte units (the
-// larger rows' registers would cost the others their blocks per SM).
-template <bool SMALL>
-__global__ void __launch_bounds__(THREADS) commit_kernel(const __grid_constant__ Args a) {
+// Block (sequence and two heads, layer).  It is latency: a chain of length,
+// path, row and write; two heads a block share the chain's start, and six
+// blocks an SM cover one another's.  (48 sequences x 32 layers x 8 heads, up to
+// 64 rows of 116 bytes each: 27 us, 3.3 TB/s, a norm's 2 bytes costing a sector
+// of 32 each way; 27.5 us with four heads a block and four blocks an SM, 42 with
+// one head, 67 with one head and divisions in the row index.)
+// SMALL: every layer's rows are of at most 64 bytes, in 16-byte units; SKETCH:
+// some layer has one (the larger rows' and the sketches' registers would cost
+// the others their blocks per SM).
+template <bool SMALL, bool SKETCH>
+__global__ void __launch_bounds__(THREADS, SMALL ? (SKETCH ? 3 : 6) : 1) commit_kernel(const __grid_constant__ Args a) {
     __shared__ long long from[MAX_PATH], to[MAX_PATH];  // cache rows of head 0 (from: -1, a row that stays)
     __shared__ int bad;
     const Layer& y = a.layers[blockIdx.y];
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(THREADS) commit_kernel(const __grid_constant__
     Mover<uint32_t, 2> kq(4 * y.qjl_words);
     kn.load(y.k_norms + row, from, n, heads, head);
     vn.load(y.v_norms + row, from, n, heads, head);
-    if (y.qjl_words) {
+    if (SKETCH && y.qjl_words) {
         kq.load(y.k_qjl + row * y.qjl_words, from, n, heads, head);
         kg.load(y.k_gamma + row, from, n, heads, head);
     }
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(THREADS) commit_kernel(const __grid_constant__
     }
     kn.store(y.k_norms + row, from, to, n, heads, head);
     vn.store(y.v_norms + row, from, to, n, heads, head);
-    if (y.qjl_words) {
+    if (SKETCH && y.qjl_words) {
         kq.store(y.k_qjl + row * y.qjl_words, from, to, n, heads, head);
         kg.store(y.k_gamma + row, from, to, n, heads, head);
     }
@@ -192,7 +193,7 @@ static tq_status commit(int32_t n_layers, const tq_params* params, const tq_cach
     }
     for (int at = 0; at < n_layers; at += LAYERS_PER_LAUNCH) {
         Args a{};
-        bool small = true;
+        bool small = true, sketch = false;
         const int count = n_layers - at < LAYERS_PER_LAUNCH ? n_layers - at : LAYERS_PER_LAUNCH;
         for (int i = 0; i < count; ++i) {
             const tq_params& p = params[at + i];
@@ -207,6 +208,7 @@ static tq_status commit(int32_t n_layers, const tq_params* params, const tq_cach
             y.k_bytes = vector_bytes(p.k_mode, p.k_bits, p.head_dim);
             y.v_bytes = vector_bytes(p.v_mode, p.v_bits, p.head_dim);
             y.qjl_words = p.qjl_dims / 32;
+            sketch = sketch || y.qjl_words;
             small = small && y.k_bytes <= 64 && y.v_bytes <= 64 && ((y.k_bytes | y.v_bytes) & 15) == 0;
             y.hkv = p.num_kv_heads;
             const int groups = (p.num_kv_heads + HEADS - 1) / HEADS;
@@ -227,8 +229,9 @@ static tq_status commit(int32_t n_layers, const tq_params* params, const tq_cach
         a.err = d_error;
         const dim3 grid(static_cast<unsigned>(batch) * a.groups, static_cast<unsigned>(count));
         cudaStream_t cs = static_cast<cudaStream_t>(stream);
-        if (small) commit_kernel<true><<<grid, THREADS, 0, cs>>>(a);
-        else commit_kernel<false><<<grid, THREADS, 0, cs>>>(a);
+        if (!small) commit_kernel<false, true><<<grid, THREADS, 0, cs>>>(a);
+        else if (sketch) commit_kernel<true, true><<<grid, THREADS, 0, cs>>>(a);
+        else commit_kernel<true, false><<<grid, THREADS, 0, cs>>>(a);
         if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
     }
     return TQ_OK;
