@@ -65,7 +65,7 @@ __device__ __forceinline__ void store8(void* base, size_t off, const float* x) {
 // fragment gives lane t the channels 32 j + 8 t .. + 7, whole 16-byte stores.
 // Centroids are fp16 at the codebook's scale (2^-11 at most); fp32 outputs add
 // a second term with what the rounding left.  (2 x 32768 tokens x 8 heads, K4
-// and V2 to bf16: 75 us, 4.2 TB/s; 132 us with all butterflies in lanes and
+// and V2 to bf16: 68 us, 4.6 TB/s; 132 us with all butterflies in lanes and
 // shuffles, bound by issue.)
 constexpr int THREADS = 256;
 
@@ -77,10 +77,17 @@ struct Table {
     uint32_t lo[LO ? 1 << (2 * BITS) : 1][32];
 };
 
-template <int D, int DTYPE, int BITS>
+template <int D, int DTYPE, int BITS, bool TOUCH>
 __device__ __forceinline__ void read_turbo(const Args& a, int side) {
     constexpr bool LO = DTYPE == 0;
     constexpr int J = D / 32;  // groups of 8 channels of a lane
+    // The next tile's rows are loaded ahead where the registers allow it (d = 64:
+    // 53.5 -> 51.4 us for 64000 tokens x 8 heads; d = 256: 101 -> 80 us for 32000).
+    // At d = 128 that spills (77 -> 89 us for 65536 tokens): there they are only
+    // touched (TOUCH, 68 us), for 16-bit outputs of a contiguous cache (a
+    // table's lookup or the second term's work cost more than it gives: 87 -> 93
+    // and 115 -> 127 us for 64000 tokens).
+    constexpr bool AHEAD = D != 128;
     extern __shared__ __align__(16) uint8_t rb_smem[];
     Table<BITS, LO>& tab = *reinterpret_cast<Table<BITS, LO>*>(rb_smem);
     const QuantSide& s = a.side[side];
@@ -136,6 +143,17 @@ __device__ __forceinline__ void read_turbo(const Args& a, int side) {
     bool ok[2];
     uint16_t nraw[2];
     uint32_t lo[2][J], hi[2][BITS == 3 ? J : 1];  // the lane's codes of group j (3 bits: in two words)
+    auto touch = [&](uint32_t w) {  // the rows of such a tile to L1
+        const uint32_t hw = w / static_cast<uint32_t>(runs);
+        const int first = static_cast<int>(w - hw * runs) * 16;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int at = start + min(first + g + 8 * r, count - 1);
+            const size_t slot = (static_cast<size_t>(b) * a.hkv + hw) * a.capacity + at;
+            if (32 * t < D * BITS / 8) asm volatile("prefetch.global.L1 [%0];" ::"l"(s.codes + slot * (D * BITS / 8) + 32 * t));
+            if (t == 3) asm volatile("prefetch.global.L1 [%0];" ::"l"(s.norms + slot));
+        }
+    };
     auto fetch = [&](uint32_t w) {  // 16 tokens of one head
         const uint32_t hw = w / static_cast<uint32_t>(runs);
         h = hw;
@@ -171,8 +189,13 @@ __device__ __forceinline__ void read_turbo(const Args& a, int side) {
             nraw[r] = s.norms[slot];
         }
     };
-    for (long long w = static_cast<long long>(blockIdx.y) * (THREADS / 32) + threadIdx.x / 32; w < tiles; w += nwarps) {
-        fetch(static_cast<uint32_t>(w));
+    long long w = static_cast<long long>(blockIdx.y) * (THREADS / 32) + threadIdx.x / 32;
+    if (AHEAD && w < tiles) fetch(static_cast<uint32_t>(w));
+    for (; w < tiles; w += nwarps) {
+        if (!AHEAD) {
+            fetch(static_cast<uint32_t>(w));
+            if (TOUCH && w + nwarps < tiles) touch(static_cast<uint32_t>(w + nwarps));
+        }
         float norm[2];
         bool live[2];
         uint32_t code[2][J];  // the 8 codes of group j, from bit 0
@@ -216,6 +239,8 @@ __device__ __forceinline__ void read_turbo(const Args& a, int side) {
                     ptx::mma_16816(acc[j][sx][1], x0, x1, x2, x3, hb[1][0], hb[1][1]);
                 }
             }
+        // the next tile's rows are on their way during the butterflies and the stores
+        if (AHEAD && w + nwarps < tiles) fetch(static_cast<uint32_t>(w + nwarps));
         // butterflies over s and the bits of j
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
@@ -346,15 +371,16 @@ __device__ __forceinline__ void read_other(const Args& a, int side) {
 }
 
 // Grid: (batch, blocks of a sequence, side).
-template <int D, int DTYPE>
+// TOUCH: see read_turbo.
+template <int D, int DTYPE, bool TOUCH>
 __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 2) read_back_kernel(const __grid_constant__ Args a) {
     const int side = static_cast<int>(blockIdx.z);
     const QuantSide& s = a.side[side];
     if (!a.out[side]) return;
     if (s.mode != TQ_MODE_TURBO || s.m > 0) read_other<D, DTYPE>(a, side);
-    else if (s.bits == 4) read_turbo<D, DTYPE, 4>(a, side);
-    else if (s.bits == 3) read_turbo<D, DTYPE, 3>(a, side);
-    else read_turbo<D, DTYPE, 2>(a, side);
+    else if (s.bits == 4) read_turbo<D, DTYPE, 4, TOUCH>(a, side);
+    else if (s.bits == 3) read_turbo<D, DTYPE, 3, TOUCH>(a, side);
+    else read_turbo<D, DTYPE, 2, TOUCH>(a, side);
 }
 
 template <int D, int DTYPE>
@@ -369,7 +395,10 @@ static cudaError_t launch_typed(Args& a, int sms, cudaStream_t s) {
         if (n > bytes) bytes = n;
     }
     // (the largest table's for every call: another thread's call may set it between this line and the launch)
-    const cudaError_t e = cudaFuncSetAttribute(read_back_kernel<D, DTYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    auto kernel = read_back_kernel<D, DTYPE, false>;
+    if constexpr (D == 128 && DTYPE != 0)
+        if (!a.table) kernel = read_back_kernel<D, DTYPE, true>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(sizeof(Table<4, DTYPE == 0>)));
     if (e != cudaSuccess) return e;
     // eight warps a block and 16 vectors a warp, two blocks an SM and side, shared by the sequences
@@ -377,7 +406,7 @@ static cudaError_t launch_typed(Args& a, int sms, cudaStream_t s) {
     const long long most = (2ll * sms + a.batch - 1) / a.batch;
     const dim3 grid(static_cast<unsigned>(a.batch), static_cast<unsigned>(want < most ? want : most), 2);
     a.copies_log2 = want <= most ? 2 : 5;
-    read_back_kernel<D, DTYPE><<<grid, THREADS, bytes, s>>>(a);
+    kernel<<<grid, THREADS, bytes, s>>>(a);
     return cudaGetLastError();
 }
 

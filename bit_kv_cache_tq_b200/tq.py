@@ -462,8 +462,8 @@ def _cache_ref(cache):
 
 
 def _check_int32(t, n, name):
-    if not (t.dtype is torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == n):
-        raise ValueError("%s: a contiguous int32 CUDA tensor of %d elements is wanted" % (name, n))
+    if not (t.dtype is torch.int32 and t.is_contiguous() and t.numel() == n):
+        raise ValueError("%s: a contiguous int32 tensor of %d elements is wanted" % (name, n))
 
 
 def _ref(struct):
@@ -550,9 +550,9 @@ def _tree_call(params, kcb, vcb, q, tree_mask, base_lens, draft_lens, cache, bat
         raise ValueError("out: a contiguous tensor of q's shape is wanted")
     if not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous tensor is wanted")
-    if not (tree_mask.dtype is torch.int64 and tree_mask.is_cuda and tree_mask.is_contiguous()
+    if not (tree_mask.dtype is torch.int64 and tree_mask.is_contiguous()
             and tree_mask.shape == shape[:2]):
-        raise ValueError("tree_mask: a contiguous int64 CUDA tensor [batch, n_draft] is wanted")
+        raise ValueError("tree_mask: a contiguous int64 tensor [batch, n_draft] is wanted")
     _check_int32(base_lens, batch, "base_lens")
     if draft_lens is not None:
         _check_int32(draft_lens, batch, "draft_lens")
