@@ -16,8 +16,8 @@
 // one (sequence, kv head) against tiles of BK keys, dequantised to fp16 in
 // shared memory; warp-level MMAs (m16n8k16, fp32 accumulation); the online
 // softmax in registers; the next tile's packed rows are loaded while a tile is
-// worked on.  Queries enter as two fp16 terms, so a score keeps
-// about 22 bits of its query.  The key axis is split between blocks and the
+// worked on.  Queries enter as fp16 terms: two, so that a score keeps
+// about 22 bits of its query, or one for bf16 outputs (see the other kernel).  The key axis is split between blocks and the
 // merge kernel joins the pieces.  It is bound by the latency of that chain with
 // three blocks an SM (two at d = 256): 16 drafts of 32 heads over 6000 tokens
 // take 85 us at d = 256 and 68 at d = 128 with a sketch; 4 sequences of 777 to
@@ -39,10 +39,15 @@ constexpr int GEN_BK = D == 256 ? 32 : 64;
 
 // Rows of halves padded by 8, so that the 8 rows of a fragment load fall in different banks.
 __host__ __device__ constexpr int gen_qk_stride(int d, int m) { return d + m + 8; }
-template <int D>
-constexpr size_t gen_smem(int m) {
-    return (2ull * GEN_ROWS + GEN_BK<D>) * gen_qk_stride(D, m) * 2 + GEN_BK<D> * (D + 8) * 2ull +
-           GEN_BK<D> * 8ull + 128;
+constexpr size_t gen_smem(int d, int m, int terms) {
+    const size_t bk = d == 256 ? GEN_BK<256> : GEN_BK<128>;
+    return (static_cast<size_t>(terms) * GEN_ROWS + bk) * gen_qk_stride(d, m) * 2 + bk * (d + 8) * 2 + bk * 8 + 128;
+}
+// Blocks an SM holds: what the launch bounds allow the registers, and shared memory.
+constexpr int gen_bound(int d) { return d == 256 ? 2 : 3; }
+static int gen_resident(int d, int m, int terms) {
+    const int n = static_cast<int>(227 * 1024 / (gen_smem(d, m, terms) + 1024));
+    return n < gen_bound(d) ? n : gen_bound(d);
 }
 
 __device__ __forceinline__ void ldmatrix_x2_trans(uint32_t& r0, uint32_t& r1, uint32_t addr) {
@@ -140,13 +145,13 @@ __global__ void __launch_bounds__(PREP_THREADS) tree_general_prep_kernel(const _
 }
 
 template <int D>
-__global__ void __launch_bounds__(GEN_THREADS, D == 256 ? 2 : 3) tree_general_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel(const __grid_constant__ Args a) {
     constexpr int BK = GEN_BK<D>;
     extern __shared__ __align__(16) uint8_t gsm[];
     const int m = a.qjl_dims, KD = D + m, KS = gen_qk_stride(D, m), VS = D + 8;
     __half* qh = reinterpret_cast<__half*>(gsm);
-    __half* ql = qh + GEN_ROWS * KS;
-    __half* ks = ql + GEN_ROWS * KS;
+    __half* ql = qh + GEN_ROWS * KS;  // (two terms)
+    __half* ks = qh + a.terms * GEN_ROWS * KS;
     __half* vs = ks + BK * KS;
     float* kn = reinterpret_cast<float*>(vs + BK * VS);
     float* vnorm = kn + BK;
@@ -169,11 +174,13 @@ __global__ void __launch_bounds__(GEN_THREADS, D == 256 ? 2 : 3) tree_general_ke
     {
         const uint4* src = reinterpret_cast<const uint4*>(a.prep + static_cast<size_t>(blockIdx.x) * (GEN_ROWS * 4) * KD);
         const int per_row = KD / 8;
-        for (int r = warp; r < 2 * GEN_ROWS; r += GEN_THREADS / 32)  // (rows of the first term, then of the second)
+        for (int r = warp; r < a.terms * GEN_ROWS; r += GEN_THREADS / 32)  // (rows of the first term, then of the second)
             for (int c = lane; c < per_row; c += 32)
                 copy16_async(ptx::smem_addr(qh + r * KS + 8 * c), src + r * per_row + c);
     }
     const int r0 = warp * 16 + lane / 4, r1 = r0 + 8;  // the lane's two rows
+    const bool idle = warp * 16 >= x.ntok * G;         // a warp without rows only dequantises
+    const bool two_terms = a.terms == 2;
     const uint64_t mk0 = r0 / G < x.ntok ? row_mask(a, x, x.tok0 + r0 / G) : 0ull;
     const uint64_t mk1 = r1 / G < x.ntok ? row_mask(a, x, x.tok0 + r1 / G) : 0ull;
     float o[D / 8][4], m0 = NOTHING, m1 = NOTHING, l0 = 0.f, l1 = 0.f;
@@ -234,15 +241,18 @@ __global__ void __launch_bounds__(GEN_THREADS, D == 256 ? 2 : 3) tree_general_ke
     // eight values of a packed group, as fp16 pairs
     auto values = [&](uint2 raw, int bits, const float* ct, float n) -> uint4 {
         float y[8];
-        if (bits == 8) {
+        if (bits == 8) {  // (exact as fp16; times a norm, fp16 too, one rounding)
+            const uint2 p = mma::int8_to_half(raw.x), q = mma::int8_to_half(raw.y);
+            uint4 v = make_uint4(p.x, p.y, q.x, q.y);
+            const __half2 n2 = __float2half2_rn(n);
+            __half2* h = reinterpret_cast<__half2*>(&v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                y[e] = n * static_cast<float>(static_cast<int8_t>(((e < 4 ? raw.x : raw.y) >> (8 * (e & 3))) & 0xffu));
-        } else {
-            const uint32_t codes = bits == 3 ? __funnelshift_r(raw.x, raw.y, 8 * ((3 * cg) & 3)) : raw.x;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = n * ct[(codes >> (bits * e)) & ((1u << bits) - 1u)];
+            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], n2);
+            return v;
         }
+        const uint32_t codes = bits == 3 ? __funnelshift_r(raw.x, raw.y, 8 * ((3 * cg) & 3)) : raw.x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = n * ct[(codes >> (bits * e)) & ((1u << bits) - 1u)];
         return make_uint4(ptx::pack_half2(y[0], y[1]), ptx::pack_half2(y[2], y[3]), ptx::pack_half2(y[4], y[5]),
                           ptx::pack_half2(y[6], y[7]));
     };
@@ -286,6 +296,10 @@ __global__ void __launch_bounds__(GEN_THREADS, D == 256 ? 2 : 3) tree_general_ke
         }
         __syncthreads();
         if (j + 1 < j1) fetch(j + 1);
+        if (idle) {
+            __syncthreads();
+            continue;
+        }
         // ---- scores
         float s[BK / 8][4];
 #pragma unroll
@@ -297,14 +311,17 @@ __global__ void __launch_bounds__(GEN_THREADS, D == 256 ? 2 : 3) tree_general_ke
             auto w32 = [](const __half* p) { return *reinterpret_cast<const uint32_t*>(p); };
             const uint32_t h0 = w32(qh + r0 * KS + cc), h1 = w32(qh + r1 * KS + cc), h2 = w32(qh + r0 * KS + cc + 8),
                            h3 = w32(qh + r1 * KS + cc + 8);
-            const uint32_t g0 = w32(ql + r0 * KS + cc), g1 = w32(ql + r1 * KS + cc), g2 = w32(ql + r0 * KS + cc + 8),
-                           g3 = w32(ql + r1 * KS + cc + 8);
+            uint32_t g0 = 0u, g1 = 0u, g2 = 0u, g3 = 0u;
+            if (two_terms) {
+                g0 = w32(ql + r0 * KS + cc), g1 = w32(ql + r1 * KS + cc);
+                g2 = w32(ql + r0 * KS + cc + 8), g3 = w32(ql + r1 * KS + cc + 8);
+            }
 #pragma unroll
             for (int n = 0; n < BK / 8; ++n) {
                 const __half* kp = ks + (8 * n + lane / 4) * KS + cc;
                 const uint32_t b0 = w32(kp), b1 = w32(kp + 8);
                 ptx::mma_16816(s[n], h0, h1, h2, h3, b0, b1);
-                ptx::mma_16816(s[n], g0, g1, g2, g3, b0, b1);
+                if (two_terms) ptx::mma_16816(s[n], g0, g1, g2, g3, b0, b1);
             }
         }
         // ---- online softmax, in log2 units
@@ -365,6 +382,7 @@ __global__ void __launch_bounds__(GEN_THREADS, D == 256 ? 2 : 3) tree_general_ke
         }
         __syncthreads();
     }
+    if (idle) return;
 #pragma unroll
     for (int q = 1; q < 4; q <<= 1) {
         l0 += __shfl_xor_sync(kFullMask, l0, q);
@@ -643,13 +661,16 @@ static Plan mma_plan(const tq_params& p, int batch, int n_draft, int sms, bool o
     return pl;
 }
 
-static Plan general_plan(const tq_params& p, int batch, int n_draft, int sms) {
+static Plan general_plan(const tq_params& p, int batch, int n_draft, int sms, bool one_term) {
     Plan pl{};
+    pl.terms = one_term ? 1 : 2;
     pl.tok_per_tile = GEN_ROWS / (p.num_q_heads / p.num_kv_heads);
     pl.qtiles = (n_draft + pl.tok_per_tile - 1) / pl.tok_per_tile;
     pl.units = static_cast<long long>(batch) * p.num_kv_heads * pl.qtiles;
-    // about three blocks an SM (what shared memory lets reside), fewer when the units alone fill them
-    long long n = (3ll * sms + pl.units - 1) / pl.units;
+    // one wave of the blocks that fit, no block more (a second wave of a few costs
+    // as much as the first: 35 us against @US@ for 4 sequences of 777 to 4001
+    // tokens, int8, d = 64), or a block per unit where the units alone fill it
+    const long long n = static_cast<long long>(gen_resident(p.head_dim, p.qjl_dims, pl.terms)) * sms / pl.units;
     pl.n_split = static_cast<int>(n < 1 ? 1 : n > 256 ? 256 : n);
     pl.prep_bytes = static_cast<size_t>(pl.units) * (GEN_ROWS * 4) * (p.head_dim + p.qjl_dims);
     pl.bytes = pl.prep_bytes + static_cast<size_t>(pl.units) * pl.n_split * GEN_ROWS * (p.head_dim + 2) * sizeof(float);
@@ -658,10 +679,10 @@ static Plan general_plan(const tq_params& p, int batch, int n_draft, int sms) {
 
 template <int D>
 static cudaError_t launch_general(const Args& a, cudaStream_t s) {
-    const size_t smem = gen_smem<D>(a.qjl_dims);
+    const size_t smem = gen_smem(D, a.qjl_dims, a.terms);
     // (the widest sketch's for every call: another thread's call may set it between this line and the launch)
     cudaError_t e = cudaFuncSetAttribute(tree_general_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(gen_smem<D>(D)));
+                                         static_cast<int>(gen_smem(D, D, 2)));
     if (e != cudaSuccess) return e;
     constexpr int per_block = PREP_THREADS / 32 * (32 / (D / 32));
     const long long prep = (static_cast<long long>(a.units) * GEN_ROWS + per_block - 1) / per_block;
@@ -694,7 +715,7 @@ static cudaError_t launch_mma(const Args& a, const Plan& pl, cudaStream_t s) {
 
 static Plan plan_of(const tq_params& p, int batch, int n_draft, int sms, int out_dtype) {
     return mma_supported(p) ? mma_plan(p, batch, n_draft, sms, out_dtype == TQ_BF16)
-                            : general_plan(p, batch, n_draft, sms);
+                            : general_plan(p, batch, n_draft, sms, out_dtype == TQ_BF16);
 }
 
 static tq_status attend(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const void* d_q,
