@@ -19,9 +19,10 @@
 // worked on.  Queries enter as fp16 terms: two, so that a score keeps
 // about 22 bits of its query, or one for bf16 outputs (see the other kernel).  The key axis is split between blocks and the
 // merge kernel joins the pieces.  It is bound by the latency of that chain with
-// three blocks an SM (two at d = 256): 16 drafts of 32 heads over 6000 tokens
-// take 85 us at d = 256 and 68 at d = 128 with a sketch; 4 sequences of 777 to
-// 4001 tokens, 17 drafts of 16 heads, int8, d = 64: 35 us.
+// three blocks an SM (two at d = 256), about 3000 instructions a warp and tile:
+// 16 drafts of 32 heads over 6000 tokens take 63 us at d = 256 and 51 at d = 128
+// with a sketch; 4 sequences of 777 to 4001 tokens, 17 drafts of 16 heads, int8,
+// d = 64: 33 us.
 
 #include "tree_common.cuh"
 #include "tree_mma_impl.cuh"
@@ -144,6 +145,29 @@ __global__ void __launch_bounds__(PREP_THREADS) tree_general_prep_kernel(const _
     }
 }
 
+// Tiles of one block's piece of unit x: pieces of equal length over all the
+// call's units (ragged sequences), as long as lets the pieces be one wave of
+// blocks (each unit may end in a short one), and no unit has more than n_split.
+// The whole warp calls it.
+template <int BK>
+__device__ __forceinline__ int piece_tiles(const Args& a, const Unit& x) {
+    if (a.batch == 1 || a.n_split == 1) return max(1, (x.ntiles + a.n_split - 1) / a.n_split);
+    long long total = 0;
+    for (int b = threadIdx.x & 31; b < a.batch; b += 32) {
+        const int base = a.base[b], drafts = a.draft_lens ? a.draft_lens[b] : a.n_draft;
+        if (drafts < 1 || drafts > a.n_draft || base < 0 || base > a.capacity - drafts) continue;
+        const uint32_t tiles = (static_cast<uint32_t>(base + drafts) + BK - 1) / BK;
+        total += static_cast<long long>(tiles) * ((drafts + a.tok_per_tile - 1) / a.tok_per_tile);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
+    total *= a.hkv;
+    const int room = a.wave - a.units;  // (above zero: n_split is 1 otherwise)
+    const long long even = (total + room - 1) / room;
+    const int most = (x.ntiles + a.n_split - 1) / a.n_split;
+    return max(1, even < x.ntiles ? max(static_cast<int>(even), most) : x.ntiles);
+}
+
 template <int D>
 __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel(const __grid_constant__ Args a) {
     constexpr int BK = GEN_BK<D>;
@@ -163,13 +187,11 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
     const Unit x = unit_of<BK>(a, static_cast<int>(blockIdx.x));
     const int G = a.group, split = static_cast<int>(blockIdx.y);
     float* mine = a.parts + (static_cast<size_t>(blockIdx.x) * a.n_split + split) * (GEN_ROWS * (D + 2));
-    const int j0 = static_cast<int>(static_cast<long long>(x.ntiles) * split / a.n_split);
-    const int j1 = static_cast<int>(static_cast<long long>(x.ntiles) * (split + 1) / a.n_split);
+    const int per = piece_tiles<BK>(a, x);
+    const long long start = static_cast<long long>(per) * split;
+    const int j0 = static_cast<int>(start < x.ntiles ? start : x.ntiles), j1 = x.ntiles - j0 > per ? j0 + per : x.ntiles;
     if (x.bad && x.qt == 0 && x.kv == 0 && split == 0 && tid == 0 && a.err) atomicOr(a.err, TQ_DEVERR_SEQLEN);
-    if (j1 <= j0) {
-        if (tid < GEN_ROWS) mine[GEN_ROWS * D + tid] = -INFINITY;
-        return;
-    }
+    if (j1 <= j0) return;  // (the unit has fewer pieces)
     // ---- queries, prepared by tree_general_prep_kernel
     {
         const uint4* src = reinterpret_cast<const uint4*>(a.prep + static_cast<size_t>(blockIdx.x) * (GEN_ROWS * 4) * KD);
@@ -418,7 +440,7 @@ __global__ void __launch_bounds__(GM_THREADS) tree_general_merge_kernel(const __
     // rows past the sequence's drafts are left as they are (all n_draft rows of a refused sequence are zeros)
     const int rows = x.bad ? min(a.tok_per_tile, a.n_draft - x.tok0) : x.ntok;
     const bool live = t < rows;
-    const int np = x.bad || !live ? 0 : a.n_split;
+    const int per = piece_tiles<GEN_BK<D>>(a, x), np = x.bad || !live ? 0 : (x.ntiles - 1) / per + 1;
     const float* first = a.parts + static_cast<size_t>(blockIdx.x) * a.n_split * (GEN_ROWS * (D + 2));
     auto piece = [&](int j) { return first + static_cast<size_t>(j) * (GEN_ROWS * (D + 2)); };
     float M = -INFINITY;
@@ -436,7 +458,7 @@ __global__ void __launch_bounds__(GM_THREADS) tree_general_merge_kernel(const __
             w[k] = 0.f;
             float m = -INFINITY;
             if (j < np) m = __ldcg(piece(j) + GEN_ROWS * D + r);
-            if (m > -INFINITY) {  // (an empty piece's rows were never written: they are not read)
+            if (m > -INFINITY) {
                 w[k] = ptx::ex2(m - M);
                 L = fmaf(__ldcg(piece(j) + GEN_ROWS * (D + 1) + r), w[k], L);
             }
@@ -625,7 +647,7 @@ __global__ void __launch_bounds__(MM_THREADS) tree_mma_merge_kernel(const __grid
                  a.out_dtype);
 }
 
-// Work layout of a call.  general: n_split blocks per unit of GEN_ROWS rows.
+// Work layout of a call.  general: up to n_split blocks per unit of GEN_ROWS rows.
 // Tensor-memory kernel: units of up to 128 rows, or (pair) 256 where a kv head
 // has more than 128 (its drafts spread evenly over its units), the
 // tile sequence shared by one block per SM (spread) or, past SCHED_MAX units,
@@ -633,7 +655,7 @@ __global__ void __launch_bounds__(MM_THREADS) tree_mma_merge_kernel(const __grid
 // and two partial outputs per block.
 struct Plan {
     long long units;
-    int tok_per_tile, qtiles, n_split, spread, blocks, pair, terms, part_rows;
+    int tok_per_tile, qtiles, n_split, wave, spread, blocks, pair, terms, part_rows;
     size_t prep_bytes, sched_bytes, bytes;
 };
 
@@ -667,11 +689,15 @@ static Plan general_plan(const tq_params& p, int batch, int n_draft, int sms, bo
     pl.tok_per_tile = GEN_ROWS / (p.num_q_heads / p.num_kv_heads);
     pl.qtiles = (n_draft + pl.tok_per_tile - 1) / pl.tok_per_tile;
     pl.units = static_cast<long long>(batch) * p.num_kv_heads * pl.qtiles;
-    // one wave of the blocks that fit, no block more (a second wave of a few costs
-    // as much as the first: 35 us against @US@ for 4 sequences of 777 to 4001
-    // tokens, int8, d = 64), or a block per unit where the units alone fill it
-    const long long n = static_cast<long long>(gen_resident(p.head_dim, p.qjl_dims, pl.terms)) * sms / pl.units;
-    pl.n_split = static_cast<int>(n < 1 ? 1 : n > 256 ? 256 : n);
+    // The pieces that one wave of blocks gives each unit (a second wave of a few
+    // blocks costs as much as the first: 87 against 63 us for 16 drafts over 6000
+    // tokens at d = 256), or one where the units alone fill the wave.  The longest
+    // sequences of a batch may take twice their share (see piece_tiles: 8
+    // sequences of 600 to 6000 tokens, d = 128 with a sketch, 16-token pages: 214
+    // -> 152 us), which costs one sequence alone 2 us and is left out there.
+    pl.wave = gen_resident(p.head_dim, p.qjl_dims, pl.terms) * sms;
+    const long long n = pl.wave <= pl.units ? 1 : (batch == 1 ? 1ll : 2ll) * pl.wave / pl.units;
+    pl.n_split = static_cast<int>(n > 256 ? 256 : n);
     pl.prep_bytes = static_cast<size_t>(pl.units) * (GEN_ROWS * 4) * (p.head_dim + p.qjl_dims);
     pl.bytes = pl.prep_bytes + static_cast<size_t>(pl.units) * pl.n_split * GEN_ROWS * (p.head_dim + 2) * sizeof(float);
     return pl;
@@ -796,6 +822,7 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     a.qtiles = pl.qtiles;
     a.units = static_cast<int>(pl.units);
     a.n_split = pl.n_split;
+    a.wave = pl.wave;
     a.spread = pl.spread;
     a.pair = pl.pair;
     a.terms = pl.terms;

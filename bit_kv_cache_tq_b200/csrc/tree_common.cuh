@@ -45,6 +45,7 @@ struct Args {
     int k_bits, v_bits, qjl_dims;  // 8 bits: an int8 side
     int staged_norms;              // rows of norms are 16-byte aligned every 8 slots
     int tok_per_tile, qtiles, units, n_split, spread;
+    int wave;                             // (general kernel) blocks that run at once
     int pair, terms, part_rows;           // (tensor-memory kernel) two row blocks a unit; fp16 terms of a query; rows of a slot
     float score_scale, out_scale, key_scale;
     uint32_t signs[8];
