@@ -154,7 +154,7 @@ __device__ __forceinline__ void turbo_encode_grid(const QuantSide& s, const uint
             const float g = x[8 * k + e] * inv;
             // round(g) in the low mantissa bits of g + 1.5 * 2^23 (|g| < 64)
             const uint32_t cell = grid[__float_as_uint(g + 12582912.0f) & 127u];
-            const uint32_t code = (cell & 15u) + (g > __uint_as_float(cell) ? 1u : 0u);
+            const uint32_t code = (cell & ((1u << BITS) - 1u)) + (g > __uint_as_float(cell) ? 1u : 0u);
             acc = acc * (1u << BITS) + code;
         }
         packed[k] = acc;
@@ -309,7 +309,10 @@ __device__ __forceinline__ void int8_encode(const QuantSide& s, const float (&x)
 }
 
 // Host: one side of the kernel arguments from its mode, width and codebook.
-inline void fill_side(QuantSide& s, int mode, int bits, int d, const tq_codebook* cb) {
+// tight: a grid cell gives up only the bits its code takes and rounds its
+// boundary to the nearest such pattern (off by at most 2, 4 or 8 ulp at 2, 3 and
+// 4 bits; by up to 15 otherwise).
+inline void fill_side(QuantSide& s, int mode, int bits, int d, const tq_codebook* cb, bool tight = false) {
     s.mode = mode;
     s.bits = mode == TQ_MODE_INT8 ? 8 : bits;
     s.vbytes = vector_bytes(mode, bits, d);
@@ -337,7 +340,13 @@ inline void fill_side(QuantSide& s, int mode, int bits, int d, const tq_codebook
             const float bnd = inside ? static_cast<float>(cb->boundaries[j] / w) : INFINITY;
             uint32_t bits32;
             std::memcpy(&bits32, &bnd, 4);
-            s.grid[c & 127] = (bits32 & ~15u) | below;
+            const uint32_t field = tight ? static_cast<uint32_t>(n) : 16u;
+            uint32_t cell = (bits32 & ~(field - 1u)) | below;
+            if (tight && inside) {
+                if (cell + field / 2 < bits32) cell += field;
+                else if (cell > bits32 + field / 2 && cell >= field) cell -= field;
+            }
+            s.grid[c & 127] = cell;
         }
         if (ok) s.grid_inv_w = static_cast<float>(1.0 / w);
     }

@@ -180,7 +180,7 @@ template <int D, int DTYPE, int KIND>
 __device__ __forceinline__ void run_kind(const Args& a, Shared<D>& sh, int chunk) {
     constexpr int LPV = D / 32, VPW = 32 / LPV;
     const QuantSide& s = a.side[KIND == 1];
-    // (Not for sketched keys: the grid's boundaries keep 20 bits, and a code that
+    // (Not for sketched keys: the grid's boundaries lose a few bits, and a code that
     // turns over at one changes the residual and with it several of its signs:
     // a tenth of the vector, where the code alone moves it by a fiftieth.)
     const bool grid_path = KIND < 2 && s.mode == TQ_MODE_TURBO && s.grid_inv_w > 0.0f && s.m == 0;
@@ -374,8 +374,8 @@ static tq_status append(const tq_params* params, const tq_codebook* kcb, const t
     const int sms = num_sms_current();
     if (sms <= 0) return TQ_ERR_CUDA;
     Args a{};
-    fill_side(a.side[0], p.k_mode, p.k_bits, p.head_dim, kcb);
-    fill_side(a.side[1], p.v_mode, p.v_bits, p.head_dim, vcb);
+    fill_side(a.side[0], p.k_mode, p.k_bits, p.head_dim, kcb, true);
+    fill_side(a.side[1], p.v_mode, p.v_bits, p.head_dim, vcb, true);
     a.side[0].codes = cache->k_codes;
     a.side[0].norms = cache->k_norms;
     a.side[0].qjl = cache->k_qjl;
