@@ -587,9 +587,9 @@ tq_status tq_rope_append_paged(const tq_params* params, const tq_codebook* kcb, 
  * valid.  sparse_v_threshold is not applied.  Every configuration of
  * tq_params is taken; outputs are within 2e-3 (relative L2 per row) of exact
  * attention over the stored codes, plus the rounding to out_dtype.  (bf16
- * outputs of d = 128 layers without a sketch take their queries in 11 bits, the
- * others in about 22.)  TQ_ERR_UNSUPPORTED also where the device reserves
- * another amount of shared memory per block than 1 KB (d = 128 without a sketch).
+ * outputs take their queries in 11 bits, the others in about 22.)
+ * TQ_ERR_UNSUPPORTED also where the device reserves another amount of shared
+ * memory per block than 1 KB (d = 128 without a sketch).
  */
 tq_status tq_tree_attention(const tq_params* params, const tq_codebook* kcb, const tq_codebook* vcb, const void* d_q,
                             tq_dtype q_dtype, int32_t n_draft, const uint64_t* d_mask, const int32_t* d_base_lens,
