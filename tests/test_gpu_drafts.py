@@ -822,3 +822,22 @@ def test_commit_of_layers_in_one_allocation(d, kb, vb, qjl):
                 want[:, b, :, base[b] + i] = before[m][:, b, :, base[b] + x]
         assert torch.equal(t, want), m
     assert new.tolist() == [base[b] + len(p) for b, p in enumerate(paths)]
+
+
+@pytest.mark.parametrize("d,kb,qjl,dtype", [(64, 8, 0, BF16), (128, 3, 32, FP32), (256, 4, 0, BF16)])
+def test_tree_of_one_long_and_several_short_sequences(d, kb, qjl, dtype):
+    """Pieces of equal length over a batch whose lengths are far apart, one sequence without drafts among them."""
+    layer = _layer(d, 8, 2, kb, 2, qjl)
+    bases, lens, n = [2900, 0, 1, 64, 1200, 5], [7, 7, 0, 3, 1, 7], 7
+    cache, _ = R.make_cache(layer, 6, 2912)
+    R.fill(layer, cache, None, 6, 2912, seed=d)
+    mask = R.random_tree(6, n, seed=8)
+    q = torch.randn(6, n, 8, d, generator=torch.Generator().manual_seed(d)).to(dtype)
+    out = torch.full_like(q, 7.0, device="cuda")
+    err = _tree_call(layer, q.cuda(), torch.from_numpy(mask).cuda(), bases, cache, None, out, draft_lens=lens)
+    assert tq.tq_read_device_error(err) == (tq.TQ_OK, 0)
+    want = R.tree_attention(layer, cache, q.double().numpy(), mask, bases, lens)
+    for b, m in enumerate(lens):
+        assert torch.all(out[b, m:] == 7.0)
+        if m:
+            _check_rows(out[b: b + 1, :m], want[b: b + 1, :m], dtype)
