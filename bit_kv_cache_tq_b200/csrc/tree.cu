@@ -31,8 +31,8 @@ namespace tq {
 namespace tree {
 
 constexpr int GEN_ROWS = 64, GEN_THREADS = 128;
-// weights are held as 2^(s - m + PSHIFT) <= 2^12 in fp16: those 2^26 times
-// smaller than the largest are still normal numbers
+// weights are held as 2^(s + e - m + PSHIFT) <= 2^12 in fp16 (e: value_exponent):
+// those 2^26 times smaller than the largest are still normal numbers
 constexpr float PSHIFT = 12.0f;
 
 template <int D>
@@ -261,15 +261,18 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
         }
     };
     // eight values of a packed group, as fp16 pairs
-    auto values = [&](uint2 raw, int bits, const float* ct, float n) -> uint4 {
+    auto values = [&](uint2 raw, int bits, const float* ct, float n, auto is_value) -> uint4 {
+        constexpr bool VALUE = decltype(is_value)::value;
         float y[8];
         if (bits == 8) {  // (exact as fp16; times a norm, fp16 too, one rounding)
-            const uint2 p = mma::int8_to_half(raw.x), q = mma::int8_to_half(raw.y);
+            const uint2 p = mma::int8_to_half<VALUE>(raw.x), q = mma::int8_to_half<VALUE>(raw.y);
             uint4 v = make_uint4(p.x, p.y, q.x, q.y);
-            const __half2 n2 = __float2half2_rn(n);
-            __half2* h = reinterpret_cast<__half2*>(&v);
+            if constexpr (VALUE) {
+                const __half2 n2 = __float2half2_rn(n);
+                __half2* h = reinterpret_cast<__half2*>(&v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], n2);
+                for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], n2);
+            }
             return v;
         }
         const uint32_t codes = bits == 3 ? __funnelshift_r(raw.x, raw.y, 8 * ((3 * cg) & 3)) : raw.x;
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
     for (int j = j0; j < j1; ++j) {
         const int key0 = j * BK, nk = min(BK, x.kend - key0);
         // ---- the tile to fp16: keys as centroids (norms multiply the fp32
-        // scores), values times their norms; slots past the end are zeros.
+        // scores), values times their norms and 2^-e; slots past the end are zeros.
         // (A value row that is not finite is left out of V~, where a zero
         // weight would turn it into NaN for rows that do not see it; its key's
         // score is NaN instead, for those that do.)
@@ -294,10 +297,14 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
             vnorm[tid] = fine ? vn : 0.f;
         }
         __syncthreads();
+        const float vtop = BK == 64 ? fmaxf(fabsf(vnorm[lane]), fabsf(vnorm[(lane + 32) % BK])) : fabsf(vnorm[lane]);
+        const int ve = value_exponent(__uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(vtop))));
+        const float vfactor = power_of_two(-ve);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int key = ck + KPP * i;
-            uint4 k8 = values(kraw[i], a.k_bits, cent, 1.f), v8 = values(vraw[i], a.v_bits, cent + 16, vnorm[key]);
+            uint4 k8 = values(kraw[i], a.k_bits, cent, 1.f, std::false_type());
+            uint4 v8 = values(vraw[i], a.v_bits, cent + 16, vnorm[key] * vfactor, std::true_type());
             if (key >= nk) k8 = v8 = make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4*>(ks + key * KS + 8 * cg) = k8;
             *reinterpret_cast<uint4*>(vs + key * VS + 8 * cg) = v8;
@@ -365,13 +372,12 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
             t0 = fmaxf(t0, __shfl_xor_sync(kFullMask, t0, q));
             t1 = fmaxf(t1, __shfl_xor_sync(kFullMask, t1, q));
         }
-        const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+        const float n0 = fmaxf(m0, t0 + ve), n1 = fmaxf(m1, t1 + ve);
         const float c0 = ptx::ex2(m0 - n0), c1 = ptx::ex2(m1 - n1);
-        const float f0 = PSHIFT - n0, f1 = PSHIFT - n1;
+        const float f0 = PSHIFT + ve - n0, f1 = PSHIFT + ve - n1;
         m0 = n0;
         m1 = n1;
-        l0 *= c0;
-        l1 *= c1;
+        float u0 = 0.f, u1 = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
             o[i][0] *= c0;
@@ -385,9 +391,11 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
             for (int e = 0; e < 2; ++e) {
                 s[n][e] = ptx::ex2(s[n][e] + f0);
                 s[n][2 + e] = ptx::ex2(s[n][2 + e] + f1);
-                l0 += s[n][e];
-                l1 += s[n][2 + e];
+                u0 += s[n][e];
+                u1 += s[n][2 + e];
             }
+        l0 = fmaf(l0, c0, u0 * vfactor);
+        l1 = fmaf(l1, c1, u1 * vfactor);
         // ---- O += P V
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
@@ -831,13 +839,13 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     const double rd = std::sqrt(static_cast<double>(p.head_dim));
     const double sm = p.sm_scale > 0.0f ? static_cast<double>(p.sm_scale) : 1.0 / rd;
     // key centroids enter at the codebook's fp16 scale, which rounds the table
-    // best; the values' as sqrt(d)/4 c (times the largest fp16 norm they stay
+    // best; the values' as sqrt(d)/4 c or q / 128, below one (times a norm they stay
     // below the fp16 range)
     const double ak = a.k_bits == 8 ? 1.0 : kcb->fp16_scale > 0.0 ? kcb->fp16_scale : rd;
     a.key_scale = static_cast<float>(ak);
     a.score_scale = static_cast<float>(sm * 1.4426950408889634 / ak);
     // (the tensor-memory kernel rounds the value table itself to fp16: at its codebook's scale too)
-    const double av = a.v_bits == 8 ? 1.0 : 0.25 * (mm && vcb->fp16_scale > 0.0 ? vcb->fp16_scale : rd);
+    const double av = a.v_bits == 8 ? 1.0 / 128.0 : 0.25 * (mm && vcb->fp16_scale > 0.0 ? vcb->fp16_scale : rd);
     a.out_scale = static_cast<float>(1.0 / av);
     for (int j = 0; j < 16; ++j) {
         a.kcent32[j] = a.k_bits < 8 && j < (1 << a.k_bits) ? static_cast<float>(kcb->centroids[j] * ak) : 0.f;

@@ -60,6 +60,20 @@ constexpr float NOTHING = -1e30f;
 // What a piece leaves as its reference: -inf marks rows without a weight.
 __device__ __forceinline__ float piece_reference(float m, float l) { return m <= NOTHING && l == 0.f ? -INFINITY : m; }
 
+// Value rows enter the products in fp16 as 2^-e times their norm, e one number
+// per key tile that brings the tile's largest norm to [2^14, 2^15): norms near
+// 65504 do not leave the fp16 range (int8 values enter as q / 128, turbo
+// centroids below one), and small ones keep their bits (2^-e is at most 2^15,
+// which makes the smallest norm fp16 holds, 2^-24, a normal number).  The
+// weights take the factor back, in the exponent they are made of: a row's
+// reference follows score + e, and sums of weights are counted without it.
+// (Turbo values of the tensor-memory kernel: e = 0.)
+constexpr int VALUE_E_MIN = -15;
+__device__ __forceinline__ int value_exponent(float largest_norm) {
+    return max(static_cast<int>(__float_as_uint(largest_norm) >> 23) - (127 + 14), VALUE_E_MIN);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // One unit: a run of query rows of one (sequence, kv head).
 struct Unit {
     int qt, kv, b, tok0, base, drafts, ntok, kend, ntiles;

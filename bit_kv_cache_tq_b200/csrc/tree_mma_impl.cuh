@@ -29,15 +29,21 @@
 //    aligned);
 //  * dequantisers (8 warps): codes to fp16 operand tiles (128-byte swizzle),
 //    keys (a tile ahead of values) as centroids, values as centroids times
-//    norms;
+//    norms (int8: see value_exponent; turbo values keep one factor, at which a
+//    norm of 65504 fits fp16 and rounding adds at most 2^-26 to a coordinate,
+//    which shows in rows of values whose norms are below 2^-13.  An exponent for
+//    each tile costs time in the dequantisers, which nothing hides: 113 -> 121 us
+//    for 16 sequences of 2048 to 8192 tokens, 13 drafts, K3/V2);
 //  * MMA issuer (1 warp): S = (Qhi + Qlo) K~^T (M = 128, N = 64, K = 128) and O += P V~
 //    (M = 128, N = 128, K = 64), the queries and the weights as A operands in
 //    tensor memory;
 //  * softmax (2 x 4 warps, one query row a thread): the queries are scaled by
 //    the softmax scale (log2 units), so a weight is 2^(S n - reference), n the
-//    key's norm.  There is no pass for the maximum: a row's reference is raised only when
-//    the tile's sum of weights shows that one of them may pass the fp16 range
-//    (always on a stream's first tile), and the tile is then done again.
+//    key's norm (int8 values: 2^(S n + e - reference), e the exponent of the
+//    tile's values).  There is no pass for the maximum: a row's reference is
+//    raised only when the tile's sum of weights shows that one of them may pass
+//    the fp16 range (always on a stream's first tile), and the tile is then done
+//    again.
 //
 // What bounds it is the shared-memory and tensor-memory data path: a tile of
 // 64 keys moves, in 128-byte passes, 256 for the scores, 128 for the weights
@@ -84,7 +90,7 @@ constexpr uint32_t TM_S = 128;   // 2 x fp32 scores [128][64]; (overlay) the wei
 constexpr uint32_t TM_O = 256;   // 2 x fp32 accumulators [128][128]
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long WAIT_LIMIT = 2000000000ll;  // clock cycles (~1 s)
-// Weights are 2^(s - reference + WSHIFT): 2^6 for a score at the reference,
+// Weights are 2^(s + e - reference + WSHIFT): 2^6 for a score at the reference,
 // normal fp16 numbers down to 2^-20 of that.  The reference moves when a
 // tile's sum passes WLIMIT, below which no single weight leaves the fp16 range.
 constexpr float WSHIFT = 6.0f, WLIMIT = 32768.0f;
@@ -111,7 +117,8 @@ constexpr uint32_t SM_V = SM_K + 2 * BK * D * 2;            // 2 x fp16 V~ [64][
 constexpr uint32_t SM_KNR = SM_V + 2 * BK * D * 2;          // fp16 key norms of the last four tiles
 constexpr uint32_t SM_ML = SM_KNR + 4 * BK * 2;             // float [2][2][2][128]: the streams' references and sums
 constexpr uint32_t SM_CENT = SM_ML + 8 * BM * 4;            // fp16 centroids, keys then values
-constexpr uint32_t SM_BAR = SM_CENT + 64;
+constexpr uint32_t SM_VEXP = SM_CENT + 64;                  // (int8 values) float2 (e, 2^-e) of the last four tiles
+constexpr uint32_t SM_BAR = SM_VEXP + 4 * 8;
 constexpr int B_FULL = 0, B_EMPTY = NS, B_KFULL = 2 * NS, B_KEMPTY = B_KFULL + 2, B_VFULL = B_KEMPTY + 2,
               B_VEMPTY = B_VFULL + 2, B_PV = B_VEMPTY + 2, B_SFULL = B_PV + 2, B_SEMPTY = B_SFULL + 2, B_PFULL = B_SEMPTY + 2, B_QREADY = B_PFULL + 2,
               B_FINAL = B_QREADY + 1, NBARS = B_FINAL + 1;
@@ -202,11 +209,14 @@ __device__ void build_lut(uint32_t* lut, const uint16_t* cent, int t, int nthrea
     }
 }
 
-// Four int8 bytes as two fp16 pairs: the byte with its top bit flipped is the
-// mantissa of 1024, 1152 + b; subtracting 1152 is exact.
+// Four int8 bytes q as two fp16 pairs, q or (FRACTION) q / 128: the byte with
+// its top bit flipped is the mantissa of 1024, 1152 + q, or of 8, 9 + q / 128;
+// subtracting 1152 or 9 is exact.
+template <bool FRACTION>
 __device__ __forceinline__ uint2 int8_to_half(uint32_t b) {
-    const uint32_t x = b ^ 0x80808080u, k = 0x64646464u;
-    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const uint32_t x = b ^ 0x80808080u, k = FRACTION ? 0x48484848u : 0x64646464u;
+    const __half zero = __ushort_as_half(FRACTION ? 0x4880 : 0x6480);
+    const __half2 off = __halves2half2(zero, zero);
     uint32_t lo = __byte_perm(x, k, 0x4140), hi = __byte_perm(x, k, 0x4342);
     const __half2 p = __hsub2(*reinterpret_cast<__half2*>(&lo), off), q = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
     return make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
@@ -226,10 +236,11 @@ __device__ __forceinline__ uint32_t lookup(uint32_t c, uint32_t l4) {
 
 // One operand tile [64 slots][128 channels] from a stage's rows by THREADS
 // threads: this one takes channel group dt % 16 (8 channels) of slots
-// dt / 16 + (THREADS / 16) i.  SCALE: times the slot's fp16 norm.  Slots at or
-// past nk are zeros.
+// dt / 16 + (THREADS / 16) i.  SCALE: values, times the slot's fp16 norm (and,
+// int8, the tile's factor, a pair).  Slots at or past nk are zeros.
 template <int BITS, bool SCALE, bool WIDE, uint32_t TABLE, int THREADS>
-__device__ __forceinline__ void dequant_tile(uint32_t tile, uint32_t codes, uint32_t snorms, int dt, int nk) {
+__device__ __forceinline__ void dequant_tile(uint32_t tile, uint32_t codes, uint32_t snorms, uint32_t factor,
+                                             int dt, int nk) {
     constexpr int RB = row_bytes(BITS), IT = BK * (D / 8) / THREADS, KS = THREADS / 16, B = 4;
     static_assert(IT % B == 0, "whole batches");
     const int cg = dt & 15, k0 = dt >> 4;
@@ -242,7 +253,7 @@ __device__ __forceinline__ void dequant_tile(uint32_t tile, uint32_t codes, uint
 #pragma unroll
             for (int i = 0; i < B; ++i) {
                 const uint32_t at = codes + (k0 + KS * (b + i)) * RB + 8 * cg;
-                const uint2 p = int8_to_half(ptx::lds32(at)), q = int8_to_half(ptx::lds32(at + 4));
+                const uint2 p = int8_to_half<SCALE>(ptx::lds32(at)), q = int8_to_half<SCALE>(ptx::lds32(at + 4));
                 v[i] = make_uint4(p.x, p.y, q.x, q.y);
             }
         } else {
@@ -282,7 +293,8 @@ __device__ __forceinline__ void dequant_tile(uint32_t tile, uint32_t codes, uint
                 // (a norm that is not finite: the row is zeros, its key's score NaN)
                 if ((nb & 0x7C00u) == 0x7C00u) nb = 0u;
                 const uint32_t n2 = nb | (nb << 16);
-                const __half2 f = *reinterpret_cast<const __half2*>(&n2);
+                __half2 f = *reinterpret_cast<const __half2*>(&n2);
+                if constexpr (BITS == 8) f = __hmul2(f, *reinterpret_cast<const __half2*>(&factor));
                 __half2* h = reinterpret_cast<__half2*>(&v[i]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
@@ -298,11 +310,17 @@ __device__ __forceinline__ void dequant_tile(uint32_t tile, uint32_t codes, uint
     }
 }
 
+// The exponent e of a tile's values (see value_exponent) from its nk staged
+// fp16 norms, by the whole warp.  (A norm that is not finite counts as 2^16.)
+__device__ __forceinline__ int tile_exponent(uint32_t snorms, int lane, int nk) {
+    uint32_t w = ptx::lds32(snorms + 4 * lane) & 0x7FFF7FFFu;
+    if (nk < BK) w = 2 * lane + 1 < nk ? w : 2 * lane < nk ? w & 0xFFFFu : 0u;
+    return max(static_cast<int>(__reduce_max_sync(kFullMask, max(w & 0xFFFFu, w >> 16)) >> 10) - 29, VALUE_E_MIN);
+}
+
 __device__ __forceinline__ float2 half2_float2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-
-
 
 // 8 consecutive fp32 columns of this thread's tensor-memory lane.
 __device__ __forceinline__ void ld_8cols(uint32_t taddr, float (&v)[8]) {
@@ -635,7 +653,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
         // (keys run a tile ahead of values: K~(gi + 1) waits for the scores of
         // tile gi - 1 only, V~(gi) for the P V of tile gi - 2)
         Tiles k, v;
+        int vexp = 0;  // (int8 values) the exponent of the keys' tile
         for (;;) {
+            const int e = vexp;  // and of the values' tile, the one before (at the end, the last)
             const bool more = k.next(a, smem);
             if (more) {
                 const int gi = k.gi, st = gi % NS, bf = gi & 1, nk = k.keys();
@@ -649,8 +669,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     reinterpret_cast<uint16_t*>(smem + SM_KNR)[(gi & 3) * BK + dt] =
                         dt >= nk ? uint16_t(0) : (vn & 0x7C00u) == 0x7C00u ? uint16_t(0x7E00) : kn;
                 }
+                if constexpr (VB == 8) {
+                    vexp = tile_exponent(sst + ST_VN, lane, nk);
+                    if (dt == 0)
+                        reinterpret_cast<float2*>(smem + SM_VEXP)[gi & 3] =
+                            make_float2(static_cast<float>(vexp), power_of_two(-vexp));
+                }
                 dequant_tile<KB, false, wide(KB), SMEM_WINDOW + SM_KLUT, DEQ_WARPS * 32>(
-                    sbase + SM_K + bf * (BK * D * 2), sst, 0u, dt, nk);
+                    sbase + SM_K + bf * (BK * D * 2), sst, 0u, 0u, dt, nk);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(B_KFULL + bf));
@@ -661,7 +687,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 const uint32_t sst = sbase + STAGE + st * STAGE_BYTES;
                 if (gi >= 2 && !wait(B_VEMPTY + bf, ((gi - 2) >> 1) & 1)) goto dequantised;
                 dequant_tile<VB, true, false, SMEM_WINDOW + sm_vlut(KB), DEQ_WARPS * 32>(
-                    sbase + SM_V + bf * (BK * D * 2), sst + ST_VC, sst + ST_VN, dt, v.keys());
+                    sbase + SM_V + bf * (BK * D * 2), sst + ST_VC, sst + ST_VN,
+                    static_cast<uint32_t>(15 - e) * 0x04000400u, dt, v.keys());
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -735,7 +762,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 dead = !wait(B_SFULL + g, q & 1);
                 if (dead) break;
                 tc::fence_after_sync();
-                const uint32_t kn = sbase + SM_KNR + (gi & 3) * BK * 2;
+                const uint32_t kn = sbase + SM_KNR + (gi & 3) * BK * 2, ve = sbase + SM_VEXP + (gi & 3) * 8;
                 const int key0 = (s.j0 + gi - gfirst) * BK;
                 const bool masked = key0 + BK > x.base;  // a tile with drafts: the tree's mask
                 uint32_t vis[2] = {0u, 0u};
@@ -749,7 +776,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 // the tile's weights against the present reference, and their
                 // sum (one straight run of code without the mask's test)
                 auto weigh = [&](auto with_mask) {
-                    const float2 nm2 = make_float2(WSHIFT - mref, WSHIFT - mref);
+                    const float shift = (VB == 8 ? WSHIFT + ptx::lds_f32(ve) : WSHIFT) - mref;
+                    const float2 nm2 = make_float2(shift, shift);
                     float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
                     float sc[32];
                     uint4 k8;
@@ -800,7 +828,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                             if ((v >> i) & 1u) m = fmaxf(m, sc[i] * n);
                         }
                     }
-                    const float mnew = fmaxf(m, mref), c = ptx::ex2(mref - mnew);
+                    const float mnew = fmaxf(VB == 8 ? m + ptx::lds_f32(ve) : m, mref), c = ptx::ex2(mref - mnew);
                     if (!first) {
                         // the accumulator is complete (overlay: this step's scores came after the stream's last P V)
                         if (!overlay) {
@@ -822,7 +850,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     mref = mnew;
                 }
                 if (dead) break;
-                l += sum;
+                l += VB == 8 ? sum * ptx::lds_f32(ve + 4) : sum;
                 uint32_t pd = tmem + lanes + TM_S + BK * g;
                 if (!overlay) {
                     tc::fence_before_sync();

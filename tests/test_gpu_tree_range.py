@@ -1,0 +1,78 @@
+"""Tree attention over the whole range of what a cache and its queries may
+hold, against the plain fp64 reference of drafts_ref.py: value scales and
+norms from the smallest to the largest that fp16 stores.  Tolerances as in test_gpu_drafts.py: 2e-3 relative L2
+per row and the rounding of the output.
+
+The 2e-3 covers what the operands round.  A score is a sum of d products of
+about |q| |k| / d each, so an error e of each (independent) moves it by
+e |q| |k| sm / sqrt(d): here |q| |k| sm is at most 120 (keys of norm 30 with
+lognormal channels, times 4 where norms grow), so the key table's 6e-5 (rms
+of the 4-bit table in fp16) move a weight by 6.4e-4 of itself, and a query in
+11 bits (2^-12.8 rms, bf16 outputs only, whose tolerance has 2^-8 more) by
+1.5e-3; weights and values in fp16 add 2^-12.8 each."""
+
+import numpy as np
+import pytest
+import torch
+
+import drafts_ref as R
+from bit_kv_cache_tq_b200 import tq
+from test_gpu_drafts import BF16, FP32, _check_rows, _layer, _tree_call
+
+pytestmark = pytest.mark.gpu
+
+
+def _half(t):
+    """The fp16 values of a tensor of stored norms (a view)."""
+    return t.view(torch.float16)
+
+
+def _run(layer, cache, q, mask, bases, drafts, dtype):
+    out = torch.full(q.shape, 7.0, dtype=dtype, device="cuda")
+    err = _tree_call(layer, q.cuda(), torch.from_numpy(mask).cuda(), bases, cache, None, out)
+    assert tq.tq_read_device_error(err) == (tq.TQ_OK, 0)
+    want = R.tree_attention(layer, cache, q.double().numpy(), mask, bases, [drafts] * len(bases))
+    assert np.isfinite(want).all()
+    return out, want
+
+
+# ------------------------------------------------------------------- values
+@pytest.mark.parametrize("scale", [600.0, 60000.0, 2.0 ** -22])
+@pytest.mark.parametrize("d,kb", [(128, 4), (128, 8), (64, 4), (256, 8)])
+def test_int8_values_of_any_scale(d, kb, scale):
+    """Every scale that fp16 holds (its product with a code of 127 does not fit fp16): all slots', or that of one draft
+    which only some rows see."""
+    layer = _layer(d, 8, 2, kb, 8, seed=6)
+    base, n = 150, 20
+    mask = R.random_tree(1, n, seed=5)
+    q = torch.randn(1, n, 8, d, generator=torch.Generator().manual_seed(3))
+    for where in (slice(None), base + 3):
+        cache, _ = R.make_cache(layer, 1, 190)
+        R.fill(layer, cache, None, 1, 190, seed=2)
+        _half(cache.v_norms)[0, :, where] = scale
+        for dtype in (FP32, BF16):
+            _check_rows(*_run(layer, cache, q.to(dtype), mask, [base], n, dtype), dtype)
+
+
+@pytest.mark.parametrize("power", [-20, -14, 8])
+@pytest.mark.parametrize("d,vb,qjl", [(128, 2, 0), (128, 4, 0), (64, 3, 0), (128, 2, 32), (256, 4, 0)])
+def test_turbo_values_of_any_norm(d, vb, qjl, power):
+    """Norms of all slots near 10 2^power, and every other tile's at that while the rest stay as they were.  The layers
+    of d = 128 without a sketch round a value row's rotated coordinates at one scale for all norms, by at most 2^-25 of
+    it, a scale of 2 or more (a quarter of the codebook's, which lies in [8, 16)): 2^-26 each, weights that add up to
+    one keep it there, the inverse rotation keeps the L2 norm, so a row may be off by another 2^-26 sqrt(128)."""
+    floor = 2.0 ** -26 * 128 ** 0.5 if d == 128 and not qjl else 0.0
+    layer = _layer(d, 8, 2, 3, vb, qjl, seed=6)
+    base, n = 200, 12
+    mask = R.random_tree(1, n, seed=5)
+    q = torch.randn(1, n, 8, d, generator=torch.Generator().manual_seed(3))
+    for every in (64, 128):
+        cache, _ = R.make_cache(layer, 1, 230)
+        R.fill(layer, cache, None, 1, 230, seed=2)
+        norms = _half(cache.v_norms)
+        for at in range(0, 230, every):
+            norms[:, :, at:at + 64] *= 2.0 ** power
+        for dtype in (FP32, BF16):
+            out, want = _run(layer, cache, q.to(dtype), mask, [base], n, dtype)
+            off = np.linalg.norm(out.cpu().double().numpy() - want, axis=-1)
+            assert np.all(off <= (R.H.ATTN_TOL + R.EPS[dtype]) * np.linalg.norm(want, axis=-1) + floor)
