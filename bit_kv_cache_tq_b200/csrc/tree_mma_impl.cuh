@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 tc::fence_after_sync();
                 const uint32_t kn = sbase + SM_KNR + (gi & 3) * BK * 2, ve = sbase + SM_VEXP + (gi & 3) * 8;
                 const int key0 = (s.j0 + gi - gfirst) * BK;
-                const bool masked = key0 + BK > x.base;  // a tile with drafts: the tree's mask
+                const bool masked = key0 > x.base - BK;  // a tile with drafts: the tree's mask (key0 + BK may pass int32)
                 uint32_t vis[2] = {0u, 0u};
                 if (masked) {
                     const uint64_t v = visible(mask, key0, x.base);

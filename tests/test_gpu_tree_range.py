@@ -1,6 +1,7 @@
 """Tree attention over the whole range of what a cache and its queries may
 hold, against the plain fp64 reference of drafts_ref.py: value scales and
-norms from the smallest to the largest that fp16 stores.  Tolerances as in test_gpu_drafts.py: 2e-3 relative L2
+norms from the smallest to the largest that fp16 stores, slots at the end of
+the int32 range.  Tolerances as in test_gpu_drafts.py: 2e-3 relative L2
 per row and the rounding of the output.
 
 The 2e-3 covers what the operands round.  A score is a sum of d products of
@@ -76,3 +77,37 @@ def test_turbo_values_of_any_norm(d, vb, qjl, power):
             out, want = _run(layer, cache, q.to(dtype), mask, [base], n, dtype)
             off = np.linalg.norm(out.cpu().double().numpy() - want, axis=-1)
             assert np.all(off <= (R.H.ATTN_TOL + R.EPS[dtype]) * np.linalg.norm(want, axis=-1) + floor)
+
+
+# ---------------------------------------------------------------- positions
+def test_drafts_in_the_last_tile_of_the_int32_range():
+    """A paged sequence of 2^31 - 16 slots (one block of zeros named again and again, then one with the drafts): each
+    draft sees the slots before the tree and itself, and its query is closest to the next draft's key, which it does
+    not see.  Its own score is 60 above the zeros' (2^31 of them weigh less than e^-38), so its output is its value."""
+    layer = _layer(128, 1, 1, 2, 2, seed=6)
+    block, per, n = 16 * 262657, 511, 20
+    base = block * per - n
+    assert block * per == 2 ** 31 - 16
+    pool = tq.alloc_cache(layer.params, 2, block)
+    table = torch.zeros(1, per, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(1, n, 1, 128, generator=g) for _ in "kv")
+    R.append(layer, pool, torch.ones(1, 1, dtype=torch.int32, device="cuda"), k.cuda(), v.cuda(), [block - n])
+    q = 12.0 * (k + 1.5 * k.roll(-1, 1))
+
+    class Last:
+        batch, capacity = 1, n
+    last = Last()
+    for name in ("k_codes", "k_norms", "v_codes", "v_norms"):
+        setattr(last, name, getattr(pool, name)[1:, :, block - n:])
+    mask = torch.tensor([[1 << t for t in range(n)]], dtype=torch.int64)
+    want = R.tree_attention(layer, last, q.double().numpy(), mask.numpy(), [0], [n])
+    scores = np.einsum("td,td->t", q[0, :, 0].double().numpy(),
+                       R.H.stored_hat(layer, last, 0, 0, n, 0)) / np.sqrt(128.0)
+    assert scores.min() > 60.0
+    for dtype in (FP32, BF16):
+        out = torch.full(q.shape, 7.0, dtype=dtype, device="cuda")
+        err = _tree_call(layer, q.to(dtype).cuda(), mask.cuda(), [base], pool, table, out)
+        assert tq.tq_read_device_error(err) == (tq.TQ_OK, 0)
+        _check_rows(out, want, dtype)
