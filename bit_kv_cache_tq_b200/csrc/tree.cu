@@ -60,8 +60,8 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
 }
 
 // The general kernel's queries, once a call: rotated (turbo keys), times the
-// softmax scale in log2 units, the sketch's projections appended, as two fp16
-// terms: per unit [2][64 rows][d + m].  A row on d / 32 lanes; blockIdx.y
+// softmax scale in log2 units (and a power of two: see row_exponent), the
+// sketch's projections appended, as two fp16 terms: per unit [2][64 rows][d + m].  A row on d / 32 lanes; blockIdx.y
 // takes PREP_SKETCH of the sketch's rows (the first also the rotated row).
 constexpr int PREP_THREADS = 128, PREP_SKETCH = 8;
 template <int D>
@@ -98,16 +98,22 @@ __global__ void __launch_bounds__(PREP_THREADS) tree_general_prep_kernel(const _
         fwht_lanes<32, LPV>(v, sub);
         scale *= rsqrtf(static_cast<float>(D));
     }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(v[i]));
+    const int k2 = row_exponent(group_max<LPV>(top) * scale);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = v[i] * scale * power_of_two(-k2);
     __half* hi = reinterpret_cast<__half*>(a.prep + static_cast<size_t>(u) * (GEN_ROWS * 4) * KD) + static_cast<size_t>(r) * KD;
     __half* lo = hi + static_cast<size_t>(GEN_ROWS) * KD;
-    auto limit = [](float y) { return fabsf(y) > mma::QLIMIT ? copysignf(mma::QLIMIT, y) : y; };  // (NaN stays)
     if (blockIdx.y == 0) {
+        if (sub == 0) a.row_factor[row] = power_of_two(k2);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint32_t hw[4], lw[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float v0 = limit(v[8 * k + 2 * e] * scale), v1 = limit(v[8 * k + 2 * e + 1] * scale);
+                const float v0 = v[8 * k + 2 * e], v1 = v[8 * k + 2 * e + 1];
                 hw[e] = ptx::pack_half2(v0, v1);
                 const float2 h = mma::half2_float2(hw[e]);
                 lw[e] = ptx::pack_half2(v0 - h.x, v1 - h.y);
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(PREP_THREADS) tree_general_prep_kernel(const _
     }
     // a key's sketch channels hold +-gamma, its others centroids times
     // key_scale (which score_scale takes out): the projections put it back
-    const float coef = m ? sqrtf(0.5f * 3.14159265358979f) / m * a.key_scale * scale : 0.f;
+    const float coef = m ? sqrtf(0.5f * 3.14159265358979f) / m * a.key_scale : 0.f;
     const int s0 = static_cast<int>(blockIdx.y) * PREP_SKETCH;
 #pragma unroll 2
     for (int j = s0; j < min(m, s0 + PREP_SKETCH); ++j) {
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(PREP_THREADS) tree_general_prep_kernel(const _
             y = fmaf(q.z, v[8 * k + 6], y);
             y = fmaf(q.w, v[8 * k + 7], y);
         }
-        y = limit(group_sum<LPV>(y) * coef);
+        y = group_sum<LPV>(y) * coef;
         if (sub == 0) {
             const __half h = __float2half_rn(y);
             hi[D + j] = h;
@@ -205,6 +211,9 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
     const bool two_terms = a.terms == 2;
     const uint64_t mk0 = r0 / G < x.ntok ? row_mask(a, x, x.tok0 + r0 / G) : 0ull;
     const uint64_t mk1 = r1 / G < x.ntok ? row_mask(a, x, x.tok0 + r1 / G) : 0ull;
+    // what the lane's rows' scores are multiplied by
+    const float* factors = a.row_factor + static_cast<size_t>(blockIdx.x) * GEN_ROWS;
+    const float g0 = factors[r0], g1 = factors[r1];
     float o[D / 8][4], m0 = NOTHING, m1 = NOTHING, l0 = 0.f, l1 = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
@@ -261,18 +270,15 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
         }
     };
     // eight values of a packed group, as fp16 pairs
-    auto values = [&](uint2 raw, int bits, const float* ct, float n, auto is_value) -> uint4 {
-        constexpr bool VALUE = decltype(is_value)::value;
+    auto values = [&](uint2 raw, int bits, const float* ct, float n) -> uint4 {
         float y[8];
         if (bits == 8) {  // (exact as fp16; times a norm, fp16 too, one rounding)
-            const uint2 p = mma::int8_to_half<VALUE>(raw.x), q = mma::int8_to_half<VALUE>(raw.y);
+            const uint2 p = mma::int8_to_half(raw.x), q = mma::int8_to_half(raw.y);
             uint4 v = make_uint4(p.x, p.y, q.x, q.y);
-            if constexpr (VALUE) {
-                const __half2 n2 = __float2half2_rn(n);
-                __half2* h = reinterpret_cast<__half2*>(&v);
+            const __half2 n2 = __float2half2_rn(n);
+            __half2* h = reinterpret_cast<__half2*>(&v);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], n2);
-            }
+            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], n2);
             return v;
         }
         const uint32_t codes = bits == 3 ? __funnelshift_r(raw.x, raw.y, 8 * ((3 * cg) & 3)) : raw.x;
@@ -303,8 +309,8 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int key = ck + KPP * i;
-            uint4 k8 = values(kraw[i], a.k_bits, cent, 1.f, std::false_type());
-            uint4 v8 = values(vraw[i], a.v_bits, cent + 16, vnorm[key] * vfactor, std::true_type());
+            uint4 k8 = values(kraw[i], a.k_bits, cent, 1.f);
+            uint4 v8 = values(vraw[i], a.v_bits, cent + 16, vnorm[key] * vfactor);
             if (key >= nk) k8 = v8 = make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4*>(ks + key * KS + 8 * cg) = k8;
             *reinterpret_cast<uint4*>(vs + key * VS + 8 * cg) = v8;
@@ -340,17 +346,17 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
             auto w32 = [](const __half* p) { return *reinterpret_cast<const uint32_t*>(p); };
             const uint32_t h0 = w32(qh + r0 * KS + cc), h1 = w32(qh + r1 * KS + cc), h2 = w32(qh + r0 * KS + cc + 8),
                            h3 = w32(qh + r1 * KS + cc + 8);
-            uint32_t g0 = 0u, g1 = 0u, g2 = 0u, g3 = 0u;
+            uint32_t y0 = 0u, y1 = 0u, y2 = 0u, y3 = 0u;
             if (two_terms) {
-                g0 = w32(ql + r0 * KS + cc), g1 = w32(ql + r1 * KS + cc);
-                g2 = w32(ql + r0 * KS + cc + 8), g3 = w32(ql + r1 * KS + cc + 8);
+                y0 = w32(ql + r0 * KS + cc), y1 = w32(ql + r1 * KS + cc);
+                y2 = w32(ql + r0 * KS + cc + 8), y3 = w32(ql + r1 * KS + cc + 8);
             }
 #pragma unroll
             for (int n = 0; n < BK / 8; ++n) {
                 const __half* kp = ks + (8 * n + lane / 4) * KS + cc;
                 const uint32_t b0 = w32(kp), b1 = w32(kp + 8);
                 ptx::mma_16816(s[n], h0, h1, h2, h3, b0, b1);
-                if (two_terms) ptx::mma_16816(s[n], g0, g1, g2, g3, b0, b1);
+                if (two_terms) ptx::mma_16816(s[n], y0, y1, y2, y3, b0, b1);
             }
         }
         // ---- online softmax, in log2 units
@@ -362,8 +368,8 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
             for (int e = 0; e < 2; ++e) {
                 const int key = 8 * n + 2 * (lane & 3) + e;
                 const float kk = kn[key];
-                s[n][e] = key < nk && ((v0 >> key) & 1u) ? s[n][e] * kk : -INFINITY;
-                s[n][2 + e] = key < nk && ((v1 >> key) & 1u) ? s[n][2 + e] * kk : -INFINITY;
+                s[n][e] = key < nk && ((v0 >> key) & 1u) ? __fmul_rn(s[n][e] * g0, kk) : -INFINITY;
+                s[n][2 + e] = key < nk && ((v1 >> key) & 1u) ? __fmul_rn(s[n][2 + e] * g1, kk) : -INFINITY;
                 t0 = fmaxf(t0, s[n][e]);
                 t1 = fmaxf(t1, s[n][2 + e]);
             }
@@ -389,8 +395,10 @@ __global__ void __launch_bounds__(GEN_THREADS, gen_bound(D)) tree_general_kernel
         for (int n = 0; n < BK / 8; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                s[n][e] = ptx::ex2(s[n][e] + f0);
-                s[n][2 + e] = ptx::ex2(s[n][2 + e] + f1);
+                // (scores past 2^25 leave more than the four bits between the largest weight and fp16's)
+                const float x0 = __fadd_rn(s[n][e], f0), x1 = __fadd_rn(s[n][2 + e], f1);
+                s[n][e] = ptx::ex2(x0 > 15.5f ? 15.5f : x0);  // (NaN stays)
+                s[n][2 + e] = ptx::ex2(x1 > 15.5f ? 15.5f : x1);
                 u0 += s[n][e];
                 u1 += s[n][2 + e];
             }
@@ -511,8 +519,9 @@ __global__ void __launch_bounds__(GM_THREADS) tree_general_merge_kernel(const __
 }
 
 // The queries of the tensor-memory kernel, once a call: rotated (turbo keys),
-// times the softmax scale and the inverse key-table scale in log2 units, as
-// one or two fp16 terms in the order its threads load them.  A row on 4 lanes,
+// times the softmax scale and the inverse key-table scale in log2 units (and a
+// power of two: see row_exponent), as one or two fp16 terms in the order its
+// threads load them.  A row on 4 lanes,
 // 32 channels each (the chunks of the encoders), 8 rows a warp.
 __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ Args a) {
     constexpr int D = mma::D, LPV = D / 32;
@@ -547,15 +556,19 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
         fwht_lanes<32, LPV>(x, sub);
         scale *= 0.08838834764831845f;  // 1 / sqrt(128)
     }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
+    const int k2 = row_exponent(group_max<LPV>(top) * scale);
+    const float shrink = power_of_two(-k2);
+    if (sub == 0) a.row_factor[row] = power_of_two(k2);
     uint4* dst = reinterpret_cast<uint4*>(a.prep + static_cast<size_t>(u) * mma::prep_bytes(a.part_rows, a.terms)) + ur;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float v0 = x[8 * k + 2 * e] * scale, v1 = x[8 * k + 2 * e + 1] * scale;
-            if (fabsf(v0) > mma::QLIMIT) v0 = copysignf(mma::QLIMIT, v0);  // (NaN stays)
-            if (fabsf(v1) > mma::QLIMIT) v1 = copysignf(mma::QLIMIT, v1);
+            const float v0 = x[8 * k + 2 * e] * scale * shrink, v1 = x[8 * k + 2 * e + 1] * scale * shrink;
             hi[e] = ptx::pack_half2(v0, v1);
             const float2 h = mma::half2_float2(hi[e]);
             lo[e] = ptx::pack_half2(v0 - h.x, v1 - h.y);
@@ -664,7 +677,7 @@ __global__ void __launch_bounds__(MM_THREADS) tree_mma_merge_kernel(const __grid
 struct Plan {
     long long units;
     int tok_per_tile, qtiles, n_split, wave, spread, blocks, pair, terms, part_rows;
-    size_t prep_bytes, sched_bytes, bytes;
+    size_t prep_bytes, factor_bytes, sched_bytes, bytes;  // (the rows' factors end the prepared queries)
 };
 
 static bool mma_supported(const tq_params& p) { return p.head_dim == mma::D && p.qjl_dims == 0; }
@@ -682,7 +695,8 @@ static Plan mma_plan(const tq_params& p, int batch, int n_draft, int sms, bool o
     pl.units = static_cast<long long>(batch) * p.num_kv_heads * pl.qtiles;
     pl.spread = pl.units <= mma::SCHED_MAX;
     pl.blocks = pl.spread ? sms : static_cast<int>(pl.units);
-    pl.prep_bytes = static_cast<size_t>(pl.units) * mma::prep_bytes(pl.part_rows, pl.terms);
+    pl.factor_bytes = static_cast<size_t>(pl.units) * pl.part_rows * sizeof(float);
+    pl.prep_bytes = static_cast<size_t>(pl.units) * mma::prep_bytes(pl.part_rows, pl.terms) + pl.factor_bytes;
     pl.bytes = pl.prep_bytes;
     if (pl.spread) {
         pl.sched_bytes = (static_cast<size_t>(pl.units + 1) * 4 + 255) / 256 * 256;
@@ -706,7 +720,8 @@ static Plan general_plan(const tq_params& p, int batch, int n_draft, int sms, bo
     pl.wave = gen_resident(p.head_dim, p.qjl_dims, pl.terms) * sms;
     const long long n = pl.wave <= pl.units ? 1 : (batch == 1 ? 1ll : 2ll) * pl.wave / pl.units;
     pl.n_split = static_cast<int>(n > 256 ? 256 : n);
-    pl.prep_bytes = static_cast<size_t>(pl.units) * (GEN_ROWS * 4) * (p.head_dim + p.qjl_dims);
+    pl.factor_bytes = static_cast<size_t>(pl.units) * GEN_ROWS * sizeof(float);
+    pl.prep_bytes = static_cast<size_t>(pl.units) * (GEN_ROWS * 4) * (p.head_dim + p.qjl_dims) + pl.factor_bytes;
     pl.bytes = pl.prep_bytes + static_cast<size_t>(pl.units) * pl.n_split * GEN_ROWS * (p.head_dim + 2) * sizeof(float);
     return pl;
 }
@@ -806,6 +821,7 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     a.out = d_out;
     a.err = d_error;
     a.prep = static_cast<uint8_t*>(d_workspace);
+    a.row_factor = reinterpret_cast<float*>(a.prep + pl.prep_bytes - pl.factor_bytes);
     a.sched = reinterpret_cast<uint32_t*>(a.prep + pl.prep_bytes);
     a.parts = reinterpret_cast<float*>(a.prep + pl.prep_bytes + pl.sched_bytes);
     a.capacity = capacity;
@@ -841,7 +857,8 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     // key centroids enter at the codebook's fp16 scale, which rounds the table
     // best; the values' as sqrt(d)/4 c or q / 128, below one (times a norm they stay
     // below the fp16 range)
-    const double ak = a.k_bits == 8 ? 1.0 : kcb->fp16_scale > 0.0 ? kcb->fp16_scale : rd;
+    const double ak = a.k_bits == 8 ? 1.0 / 128.0
+                                    : (kcb->fp16_scale > 0.0 ? kcb->fp16_scale : rd) * (mm ? mma::KEY_SHIFT : 1.0);
     a.key_scale = static_cast<float>(ak);
     a.score_scale = static_cast<float>(sm * 1.4426950408889634 / ak);
     // (the tensor-memory kernel rounds the value table itself to fp16: at its codebook's scale too)

@@ -37,7 +37,8 @@ struct Args {
     uint32_t* err;
     float* parts;                // partial results (see the kernels)
     uint32_t* sched;             // [units + 1] (tensor-memory kernel)
-    uint8_t* prep;               // prepared queries (tensor-memory kernel)
+    uint8_t* prep;               // prepared queries
+    float* row_factor;           // [units][rows] what their scores are multiplied by (see row_exponent)
     const int32_t* table;        // paged, or null
     int max_blocks, block_size, num_blocks;
     uint64_t block_magic;        // ceil(2^64 / block_size): t / block_size is the high word of t times it
@@ -56,7 +57,7 @@ struct Args {
 // A row's softmax reference before it has seen a key: below every score, but
 // finite, so that masked scores (-inf) weigh 2^-inf = 0 against it and a NaN
 // score stays NaN.
-constexpr float NOTHING = -1e30f;
+constexpr float NOTHING = -0x1p127f;
 // What a piece leaves as its reference: -inf marks rows without a weight.
 __device__ __forceinline__ float piece_reference(float m, float l) { return m <= NOTHING && l == 0.f ? -INFINITY : m; }
 
@@ -73,6 +74,15 @@ __device__ __forceinline__ int value_exponent(float largest_norm) {
     return max(static_cast<int>(__float_as_uint(largest_norm) >> 23) - (127 + 14), VALUE_E_MIN);
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Prepared queries are fp16 terms of 2^-k times the row, k = 0 for rows whose
+// largest entry lies in [2^-2, 2^15) (entries 2^-23 of it and below are lost, no
+// more than two terms hold) and else the exponent of that entry: no query is
+// cut, none loses its bits.  The scores are multiplied by 2^k in fp32.
+__device__ __forceinline__ int row_exponent(float largest) {
+    if (!(largest > 0.f && largest < INFINITY) || (largest >= 0.25f && largest < 32768.f)) return 0;
+    return min(max(static_cast<int>(__float_as_uint(largest) >> 23) - 127, -126), 126);
+}
 
 // One unit: a run of query rows of one (sequence, kv head).
 struct Unit {

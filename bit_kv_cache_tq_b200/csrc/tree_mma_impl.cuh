@@ -93,8 +93,10 @@ constexpr long long WAIT_LIMIT = 2000000000ll;  // clock cycles (~1 s)
 // Weights are 2^(s + e - reference + WSHIFT): 2^6 for a score at the reference,
 // normal fp16 numbers down to 2^-20 of that.  The reference moves when a
 // tile's sum passes WLIMIT, below which no single weight leaves the fp16 range.
-constexpr float WSHIFT = 6.0f, WLIMIT = 32768.0f;
-constexpr float QLIMIT = 60000.0f;  // scaled queries past the fp16 range are cut (their scores pass 10^4 either way)
+constexpr float WSHIFT = 6.0f, WLIMIT = 32768.0f, WMOST = 15.5f;
+// The key table is 2^-8 of the codebook's fp16 scale (int8 keys: q / 128), so
+// that ordinary queries, which carry the inverse, need no factor of their own.
+constexpr double KEY_SHIFT = 1.0 / 256.0;
 
 // Prepared queries of a unit: per fp16 term, 16 chunks of 8 channels of every
 // row, the rows of a chunk next to each other.
@@ -118,7 +120,8 @@ constexpr uint32_t SM_KNR = SM_V + 2 * BK * D * 2;          // fp16 key norms of
 constexpr uint32_t SM_ML = SM_KNR + 4 * BK * 2;             // float [2][2][2][128]: the streams' references and sums
 constexpr uint32_t SM_CENT = SM_ML + 8 * BM * 4;            // fp16 centroids, keys then values
 constexpr uint32_t SM_VEXP = SM_CENT + 64;                  // (int8 values) float2 (e, 2^-e) of the last four tiles
-constexpr uint32_t SM_BAR = SM_VEXP + 4 * 8;
+constexpr uint32_t SM_FACTOR = SM_VEXP + 4 * 8;             // float [256]: the softmax threads' row factors
+constexpr uint32_t SM_BAR = SM_FACTOR + SOFTMAX_WARPS * 32 * 4;
 constexpr int B_FULL = 0, B_EMPTY = NS, B_KFULL = 2 * NS, B_KEMPTY = B_KFULL + 2, B_VFULL = B_KEMPTY + 2,
               B_VEMPTY = B_VFULL + 2, B_PV = B_VEMPTY + 2, B_SFULL = B_PV + 2, B_SEMPTY = B_SFULL + 2, B_PFULL = B_SEMPTY + 2, B_QREADY = B_PFULL + 2,
               B_FINAL = B_QREADY + 1, NBARS = B_FINAL + 1;
@@ -209,14 +212,11 @@ __device__ void build_lut(uint32_t* lut, const uint16_t* cent, int t, int nthrea
     }
 }
 
-// Four int8 bytes q as two fp16 pairs, q or (FRACTION) q / 128: the byte with
-// its top bit flipped is the mantissa of 1024, 1152 + q, or of 8, 9 + q / 128;
-// subtracting 1152 or 9 is exact.
-template <bool FRACTION>
+// Four int8 bytes q as two fp16 pairs q / 128: the byte with its top bit
+// flipped is the mantissa of 8, 9 + q / 128; subtracting 9 is exact.
 __device__ __forceinline__ uint2 int8_to_half(uint32_t b) {
-    const uint32_t x = b ^ 0x80808080u, k = FRACTION ? 0x48484848u : 0x64646464u;
-    const __half zero = __ushort_as_half(FRACTION ? 0x4880 : 0x6480);
-    const __half2 off = __halves2half2(zero, zero);
+    const uint32_t x = b ^ 0x80808080u, k = 0x48484848u;
+    const __half2 off = __halves2half2(__ushort_as_half(0x4880), __ushort_as_half(0x4880));
     uint32_t lo = __byte_perm(x, k, 0x4140), hi = __byte_perm(x, k, 0x4342);
     const __half2 p = __hsub2(*reinterpret_cast<__half2*>(&lo), off), q = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
     return make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
@@ -253,7 +253,7 @@ __device__ __forceinline__ void dequant_tile(uint32_t tile, uint32_t codes, uint
 #pragma unroll
             for (int i = 0; i < B; ++i) {
                 const uint32_t at = codes + (k0 + KS * (b + i)) * RB + 8 * cg;
-                const uint2 p = int8_to_half<SCALE>(ptx::lds32(at)), q = int8_to_half<SCALE>(ptx::lds32(at + 4));
+                const uint2 p = int8_to_half(ptx::lds32(at)), q = int8_to_half(ptx::lds32(at + 4));
                 v[i] = make_uint4(p.x, p.y, q.x, q.y);
             }
         } else {
@@ -542,7 +542,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                             n[h] = k < nk ? a.k_norms[row + k] : uint16_t(0);
                             n[2 + h] = k < nk ? a.v_norms[row + k] : uint16_t(0);
                         }
-                        if (gi >= NS && !wait(B_EMPTY + st, ((gi - NS) / NS) & 1)) goto norms_done;
+                        // (polling would take issue slots from the working warps)
+                        if (gi >= NS && !ptx::mbar_wait_bounded_sleep(bar(B_EMPTY + st), ((gi - NS) / NS) & 1, WAIT_LIMIT, 64)) {
+                            fail();
+                            goto norms_done;
+                        }
                         uint16_t* kn = reinterpret_cast<uint16_t*>(smem + STAGE + st * STAGE_BYTES + ST_KN);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -748,6 +752,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     tc::st_16cols_u(dst + 4 * c, v);
                 }
             }
+            // a warp with a row whose scores are multiplied by a factor, or pass
+            // 2^22, takes the masked path for all its tiles
+            int careful_from = x.base - BK;
+            {
+                const float f = a.row_factor[static_cast<size_t>(s.u) * a.part_rows + ur];
+                *reinterpret_cast<float*>(smem + SM_FACTOR + 4 * tid) = f;
+                if (__any_sync(kFullMask, f != 1.f)) careful_from = -1;
+            }
             tc::st_wait();
             tc::fence_before_sync();
             __syncwarp();
@@ -764,18 +776,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 tc::fence_after_sync();
                 const uint32_t kn = sbase + SM_KNR + (gi & 3) * BK * 2, ve = sbase + SM_VEXP + (gi & 3) * 8;
                 const int key0 = (s.j0 + gi - gfirst) * BK;
-                const bool masked = key0 > x.base - BK;  // a tile with drafts: the tree's mask (key0 + BK may pass int32)
-                uint32_t vis[2] = {0u, 0u};
-                if (masked) {
-                    const uint64_t v = visible(mask, key0, x.base);
-                    vis[0] = static_cast<uint32_t>(v);
-                    vis[1] = static_cast<uint32_t>(v >> 32);
-                }
                 uint32_t pw[BK / 2];
                 float sum;
                 // the tile's weights against the present reference, and their
-                // sum (one straight run of code without the mask's test)
+                // sum (one straight run of code without the mask's test and the
+                // rows' factors)
                 auto weigh = [&](auto with_mask) {
+                    const float f = decltype(with_mask)::value ? ptx::lds_f32(sbase + SM_FACTOR + 4 * tid) : 1.f;
+                    const uint64_t seen = decltype(with_mask)::value ? visible(mask, key0, x.base) : 0ull;
+                    const uint32_t vis[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
                     const float shift = (VB == 8 ? WSHIFT + ptx::lds_f32(ve) : WSHIFT) - mref;
                     const float2 nm2 = make_float2(shift, shift);
                     float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
@@ -790,9 +799,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                         if (i % 8 == 0) k8 = ptx::lds128(kn + 2 * i);  // the norms of 8 keys
                         const int e = i % 32;
                         const float2 n0 = half2_float2(i % 8 ? k8.z : k8.x), n1 = half2_float2(i % 8 ? k8.w : k8.y);
-                        float2 t0 = ptx::ffma2(make_float2(sc[e], sc[e + 1]), n0, nm2);
-                        float2 t1 = ptx::ffma2(make_float2(sc[e + 2], sc[e + 3]), n1, nm2);
-                        if constexpr (decltype(with_mask)::value) {
+                        const float2 s0 = make_float2(sc[e], sc[e + 1]), s1 = make_float2(sc[e + 2], sc[e + 3]);
+                        float2 t0, t1;
+                        if constexpr (!decltype(with_mask)::value) {
+                            t0 = ptx::ffma2(s0, n0, nm2);
+                            t1 = ptx::ffma2(s1, n1, nm2);
+                        } else {
+                            // (scores rounded as the reference was, in single operations
+                            // that are not fused, and weights that fit fp16, however large
+                            // the scores; NaN stays)
+                            auto shifted = [&](float x, float n) {
+                                const float t = __fadd_rn(__fmul_rn(__fmul_rn(x, f), n), shift);
+                                return t > WMOST ? WMOST : t;
+                            };
+                            t0 = make_float2(shifted(s0.x, n0.x), shifted(s0.y, n0.y));
+                            t1 = make_float2(shifted(s1.x, n1.x), shifted(s1.y, n1.y));
                             const uint32_t v = vis[i / 32] >> e;
                             if (!(v & 1u)) t0.x = -INFINITY;
                             if (!(v & 2u)) t0.y = -INFINITY;
@@ -810,25 +831,31 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 };
 #pragma unroll 1
                 for (bool again = false;; again = true) {
-                    if (masked) weigh(std::true_type());
+                    // (a tile with drafts: the tree's mask; key0 + BK may pass int32)
+                    const bool careful = key0 > careful_from;
+                    if (careful) weigh(std::true_type());
                     else weigh(std::false_type());
                     if (again || !__any_sync(kFullMask, !(sum <= WLIMIT))) break;
                     // a weight may leave the fp16 range (or is NaN): raise the
                     // reference to the row's largest score, rescale, again
                     float m = -INFINITY;
+                    const float f = ptx::lds_f32(sbase + SM_FACTOR + 4 * tid);
+                    const uint64_t seen = careful ? visible(mask, key0, x.base) : ~0ull;
 #pragma unroll 1
                     for (int h = 0; h < 4; ++h) {
                         float sc[16];
                         tc::ld_16cols(tmem + lanes + TM_S + BK * g + 16 * h, sc);
                         tc::ld_wait();
-                        const uint32_t v = masked ? (h < 2 ? vis[0] : vis[1]) >> (16 * (h & 1)) : ~0u;
+                        const uint32_t v = static_cast<uint32_t>(seen >> (16 * h));
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const float n = half_bits_to_float(ptx::lds16(kn + 2 * (16 * h + i)));
-                            if ((v >> i) & 1u) m = fmaxf(m, sc[i] * n);
+                            if ((v >> i) & 1u) m = fmaxf(m, __fmul_rn(__fmul_rn(sc[i], f), n));
                         }
                     }
                     const float mnew = fmaxf(VB == 8 ? m + ptx::lds_f32(ve) : m, mref), c = ptx::ex2(mref - mnew);
+                    // (past 2^22 a fused product would differ from the reference by more than a bit)
+                    if (__any_sync(kFullMask, fabsf(mnew) > 0x1p22f && mnew > NOTHING)) careful_from = -1;
                     if (!first) {
                         // the accumulator is complete (overlay: this step's scores came after the stream's last P V)
                         if (!overlay) {

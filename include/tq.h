@@ -587,7 +587,8 @@ tq_status tq_rope_append_paged(const tq_params* params, const tq_codebook* kcb, 
  * valid.  sparse_v_threshold is not applied.  Every configuration of
  * tq_params is taken; outputs are within 2e-3 (relative L2 per row) of exact
  * attention over the stored codes, plus the rounding to out_dtype.  (bf16
- * outputs take their queries in 11 bits, the others in about 22.  Turbo values
+ * outputs take their queries in 11 bits of each entry, the others in about 22
+ * of the row's largest entry, whatever its size.  Turbo values
  * of d = 128 layers without a sketch are rounded at one scale for all norms,
  * which adds up to 2^-22 (L2) to a row, whatever its size.)
  * TQ_ERR_UNSUPPORTED also where the device reserves another amount of shared

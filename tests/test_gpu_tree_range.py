@@ -1,7 +1,7 @@
 """Tree attention over the whole range of what a cache and its queries may
 hold, against the plain fp64 reference of drafts_ref.py: value scales and
-norms from the smallest to the largest that fp16 stores, slots at the end of
-the int32 range.  Tolerances as in test_gpu_drafts.py: 2e-3 relative L2
+norms from the smallest to the largest that fp16 stores, queries far from one,
+slots at the end of the int32 range.  Tolerances as in test_gpu_drafts.py: 2e-3 relative L2
 per row and the rounding of the output.
 
 The 2e-3 covers what the operands round.  A score is a sum of d products of
@@ -77,6 +77,43 @@ def test_turbo_values_of_any_norm(d, vb, qjl, power):
             out, want = _run(layer, cache, q.to(dtype), mask, [base], n, dtype)
             off = np.linalg.norm(out.cpu().double().numpy() - want, axis=-1)
             assert np.all(off <= (R.H.ATTN_TOL + R.EPS[dtype]) * np.linalg.norm(want, axis=-1) + floor)
+
+
+# ------------------------------------------------------------------ queries
+@pytest.mark.parametrize("keys", ["large", "small", "ordinary"])
+@pytest.mark.parametrize("d,kb,qjl", [(128, 4, 0), (128, 8, 0), (64, 2, 0), (128, 3, 64), (256, 8, 0)])
+def test_queries_of_any_magnitude(d, kb, qjl, keys):
+    """Small queries against keys whose norms reach 60000, large ones against keys whose norms end at 2^-14 (the scores
+    stay as they were, but for a factor below two), and rows of ordinary and of small queries next to each other: no
+    query is cut, none loses its bits."""
+    layer = _layer(d, 8, 2, kb, 4, qjl, seed=6)
+    base, n = 200, 20
+    mask = R.random_tree(1, n, seed=5)
+    q = torch.randn(1, n, 8, d, generator=torch.Generator().manual_seed(3))
+    cache, _ = R.make_cache(layer, 1, 230)
+    R.fill(layer, cache, None, 1, 230, seed=2)
+    norms = _half(cache.k_norms)[:, :, :base + n]
+    if keys == "ordinary":
+        q[:, ::3] *= 2.0 ** -10
+    else:
+        factor = (60000.0 if keys == "large" else 2.0 ** -14) / norms.float().amax().item()
+        norms.copy_(norms.float() * factor)
+        q *= 2.0 ** -np.ceil(np.log2(factor))
+    for dtype in (FP32, BF16):
+        _check_rows(*_run(layer, cache, q.to(dtype), mask, [base], n, dtype), dtype)
+
+
+@pytest.mark.parametrize("power", [-120, 100])
+@pytest.mark.parametrize("d,kb", [(128, 4), (128, 8), (64, 4)])
+def test_queries_at_the_ends_of_fp32(d, kb, power):
+    """A draft that sees itself alone gets its own value, whatever its score."""
+    layer = _layer(d, 4, 2, kb, 4, seed=6)
+    cache, _ = R.make_cache(layer, 1, 16)
+    R.fill(layer, cache, None, 1, 16, seed=2)
+    mask = np.array([[1 << t for t in range(9)]], dtype=np.int64)
+    q = torch.randn(1, 9, 4, d, generator=torch.Generator().manual_seed(3)) * 2.0 ** power
+    for dtype in (FP32, BF16):
+        _check_rows(*_run(layer, cache, q.to(dtype), mask, [0], 9, dtype), dtype)
 
 
 # ---------------------------------------------------------------- positions
