@@ -59,7 +59,8 @@
 // drafts of 64 heads (K4/V4, fp16, two terms): 470 to 520 us.
 //
 // Every mbarrier wait is bounded (about a second, then TQ_DEVERR_TIMEOUT; the
-// block stops issuing, waits for its copies and MMAs, frees tensor memory).
+// block stops issuing copies and MMAs, waits for those under way, and its other
+// warps run to the end of their tiles without waiting).
 #pragma once
 
 #include <type_traits>
@@ -346,7 +347,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
         if (!*abort_flag && a.err) atomicOr(a.err, TQ_DEVERR_TIMEOUT);
         *abort_flag = 1;
     };
-    auto wait = [&](int i, uint32_t parity) -> bool {
+    // A wait that runs out sets the flag, and once it is set no wait waits: the
+    // warps go on through their tiles as they would have (on data that is not
+    // valid), so no lane leaves its warp, nor a warp the block, at a collective
+    // instruction.  Only what would start new work stops: the producer and the
+    // MMA issuer (which alone uses the answer).
+    auto lane_wait = [&](int i, uint32_t parity) -> bool {
         const uint32_t b = bar(i);
         if (ptx::mbar_try_wait(b, parity)) return true;
         const long long start = clock64();
@@ -357,6 +363,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
             if (clock64() - start > WAIT_LIMIT) fail();
         }
         return false;
+    };
+    auto wait = [&](int i, uint32_t parity) { lane_wait(i, parity); };
+    // for warps that wait most of the time (polling would take issue slots from the working ones)
+    auto wait_asleep = [&](int i, uint32_t parity) {
+        if (!*abort_flag && !ptx::mbar_wait_bounded_sleep(bar(i), parity, WAIT_LIMIT, 64)) fail();
     };
     const int G = a.group;
     const bool pair = a.pair, two_terms = a.terms == 2, overlay = pair || two_terms;
@@ -492,11 +503,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 for (int j = s.j0; j < s.j1; ++j, ++gi) {
                     const int st = gi % NS;
                     if (gi >= NS) {
-                        if (*abort_flag) goto produced;
-                        if (!ptx::mbar_wait_bounded_sleep(bar(B_EMPTY + st), ((gi - NS) / NS) & 1, WAIT_LIMIT, 64)) {
-                            fail();
-                            goto produced;
-                        }
+                        wait_asleep(B_EMPTY + st, ((gi - NS) / NS) & 1);
+                        if (__any_sync(kFullMask, *abort_flag)) goto produced;
                     }
                     if (leader) {
                         const int key0 = j * BK, nk = min(BK, x.kend - key0), n8 = (nk + 7) & ~7;
@@ -542,11 +550,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                             n[h] = k < nk ? a.k_norms[row + k] : uint16_t(0);
                             n[2 + h] = k < nk ? a.v_norms[row + k] : uint16_t(0);
                         }
-                        // (polling would take issue slots from the working warps)
-                        if (gi >= NS && !ptx::mbar_wait_bounded_sleep(bar(B_EMPTY + st), ((gi - NS) / NS) & 1, WAIT_LIMIT, 64)) {
-                            fail();
-                            goto norms_done;
-                        }
+                        if (gi >= NS) wait_asleep(B_EMPTY + st, ((gi - NS) / NS) & 1);
                         uint16_t* kn = reinterpret_cast<uint16_t*>(smem + STAGE + st * STAGE_BYTES + ST_KN);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -558,17 +562,19 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     }
                 }
             }
-        norms_done:;
         } else if (warp == MMA_WARP) {
             // ----------------------------------------------------- MMA issuer
+            // (no collective instruction before the end of the role: after a wait
+            // that ran out, lanes may leave the loops one by one)
             const bool leader = tc::elect_one();
             const uint32_t idesc_s = tc::idesc_f16(BM, BK), idesc_o = tc::idesc_f16_bmn(BM, D);
             const uint64_t kdesc0 = tc::sw128_desc(sbase + SM_K);
             const uint64_t vdesc0 = tc::sw128_mn_desc(sbase + SM_V, BK * 128, 1024);
             // scores of stream g from tile gi; the tile's last reader frees it
+            // (false: a wait ran out somewhere, nothing is issued any more)
             auto issue_s = [&](int gi, int g, bool last) -> bool {
                 const int bf = gi & 1;
-                if (!wait(B_KFULL + bf, (gi >> 1) & 1)) return false;
+                if (!lane_wait(B_KFULL + bf, (gi >> 1) & 1)) return false;
                 tc::fence_after_sync();
                 if (leader) {
                     const uint64_t kd = kdesc0 + static_cast<uint64_t>(bf * (BK * D * 2) >> 4);
@@ -582,14 +588,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     tc::commit(bar(B_SFULL + g));
                     if (last) tc::commit(bar(B_KEMPTY + bf));
                 }
-                __syncwarp();
                 return true;
             };
             // output of stream g's step q from tile gi
             auto issue_pv = [&](int gi, int g, int q, bool first, bool last) -> bool {
                 const int bf = gi & 1;
-                if (!wait(B_PFULL + g, q & 1)) return false;
-                if (!wait(B_VFULL + bf, (gi >> 1) & 1)) return false;
+                if (!lane_wait(B_PFULL + g, q & 1)) return false;
+                if (!lane_wait(B_VFULL + bf, (gi >> 1) & 1)) return false;
                 tc::fence_after_sync();
                 if (leader) {
                     const uint64_t vd = vdesc0 + static_cast<uint64_t>(bf * (BK * D * 2) >> 4);
@@ -601,7 +606,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     tc::commit(bar(B_PV + g));
                     if (last) tc::commit(bar(B_VEMPTY + bf));
                 }
-                __syncwarp();
                 return true;
             };
             int gi = 0, qs = 0, it = -1;
@@ -609,7 +613,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
             while (next_segment(a, smem, it, s)) {
                 if (s.j1 <= s.j0) continue;
                 // the queries are in tensor memory, and the segment before has left it
-                if (!wait(B_QREADY, qs & 1)) break;
+                if (!lane_wait(B_QREADY, qs & 1)) break;
                 ++qs;
                 const int gfirst = gi, gend = gi + (s.j1 - s.j0);
                 // (overlay: a stream's weights lie in its score buffer, so its
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                         for (int g = 0; g < 2; ++g) {
                             if (!issue_pv(gi, g, gi, gi == gfirst, g == 1)) goto issued;
                             if (gi + 1 < gend) {
-                                if (!wait(B_PV + g, gi & 1)) goto issued;
+                                if (!lane_wait(B_PV + g, gi & 1)) goto issued;
                                 if (!issue_s(gi + 1, g, g == 1)) goto issued;
                             }
                         }
@@ -632,12 +636,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     for (; gi < gend; ++gi) {
                         const int g = gi & 1, q = gi >> 1;
                         if (!overlay && gi + 2 < gend) {
-                            if (!wait(B_SEMPTY + g, q & 1)) goto issued;
+                            if (!lane_wait(B_SEMPTY + g, q & 1)) goto issued;
                             if (!issue_s(gi + 2, g, true)) goto issued;
                         }
                         if (!issue_pv(gi, g, q, gi < gfirst + 2, true)) goto issued;
                         if (overlay && gi + 2 < gend) {
-                            if (!wait(B_PV + g, q & 1)) goto issued;
+                            if (!lane_wait(B_PV + g, q & 1)) goto issued;
                             if (!issue_s(gi + 2, g, true)) goto issued;
                         }
                     }
@@ -664,8 +668,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
             if (more) {
                 const int gi = k.gi, st = gi % NS, bf = gi & 1, nk = k.keys();
                 const uint32_t sst = sbase + STAGE + st * STAGE_BYTES;
-                if (!wait(B_FULL + st, (gi / NS) & 1)) goto dequantised;
-                if (gi >= 2 && !wait(B_KEMPTY + bf, ((gi - 2) >> 1) & 1)) goto dequantised;
+                wait(B_FULL + st, (gi / NS) & 1);
+                if (gi >= 2) wait(B_KEMPTY + bf, ((gi - 2) >> 1) & 1);
                 if (dt < BK) {
                     // the tile's key norms, for the softmax (which is through
                     // with tile gi - 4: the scores of tile gi - 2 followed it)
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 v.next(a, smem);
                 const int gi = v.gi, st = gi % NS, bf = gi & 1;
                 const uint32_t sst = sbase + STAGE + st * STAGE_BYTES;
-                if (gi >= 2 && !wait(B_VEMPTY + bf, ((gi - 2) >> 1) & 1)) goto dequantised;
+                if (gi >= 2) wait(B_VEMPTY + bf, ((gi - 2) >> 1) & 1);
                 dequant_tile<VB, true, false, SMEM_WINDOW + sm_vlut(KB), DEQ_WARPS * 32>(
                     sbase + SM_V + bf * (BK * D * 2), sst + ST_VC, sst + ST_VN,
                     static_cast<uint32_t>(15 - e) * 0x04000400u, dt, v.keys());
@@ -702,7 +706,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
             }
             if (!more) break;
         }
-    dequantised:;
     } else {
         // ---------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
@@ -766,13 +769,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
             if (lane == 0) ptx::mbar_arrive(bar(B_QREADY));
             const uint64_t mask = row_ok ? row_mask(a, x, x.tok0 + rt) : 0ull;
             float mref = NOTHING, l = 0.f;
-            bool dead = false, first = true;
+            bool first = true;
             const int gfirst = gi, gend = gi + (s.j1 - s.j0), inc = pair ? 1 : 2;
             if (!pair) gi += (gi & 1) != g;  // the stream's first tile of the segment
             for (; gi < gend; gi += inc, first = false) {
                 const int q = pair ? gi : gi >> 1;
-                dead = !wait(B_SFULL + g, q & 1);
-                if (dead) break;
+                wait(B_SFULL + g, q & 1);
                 tc::fence_after_sync();
                 const uint32_t kn = sbase + SM_KNR + (gi & 3) * BK * 2, ve = sbase + SM_VEXP + (gi & 3) * 8;
                 const int key0 = (s.j0 + gi - gfirst) * BK;
@@ -859,8 +861,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     if (!first) {
                         // the accumulator is complete (overlay: this step's scores came after the stream's last P V)
                         if (!overlay) {
-                            dead = !wait(B_PV + g, (q - 1) & 1);
-                            if (dead) break;
+                            wait(B_PV + g, (q - 1) & 1);
                             tc::fence_after_sync();
                         }
 #pragma unroll 1
@@ -876,7 +877,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     l *= c;
                     mref = mnew;
                 }
-                if (dead) break;
                 l += VB == 8 ? sum * ptx::lds_f32(ve + 4) : sum;
                 uint32_t pd = tmem + lanes + TM_S + BK * g;
                 if (!overlay) {
@@ -884,8 +884,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(bar(B_SEMPTY + g));  // the scores have been read
                     if (!first) {  // the weights' columns are free when the stream's last P V is done
-                        dead = !wait(B_PV + g, (q - 1) & 1);
-                        if (dead) break;
+                        wait(B_PV + g, (q - 1) & 1);
                         tc::fence_after_sync();
                     }
                     pd = tmem + lanes + TM_Q + 64 + (BK / 2) * g;
@@ -901,15 +900,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
             // the same rows are joined
             {
                 const int last = pair ? gend - 1 : gend - 1 - ((gend - 1 - g) & 1);  // the stream's last tile, if any
-                if (!dead && last >= gfirst) dead = !wait(B_PV + g, (pair ? last : last >> 1) & 1);
+                if (last >= gfirst) wait(B_PV + g, (pair ? last : last >> 1) & 1);
                 gi = gend;
                 ml += ml_next;
                 ml_next = -ml_next;
                 ml[g * BM + r] = mref;
                 ml[(2 + g) * BM + r] = l;
             }
-            // (after a wait that ran out every softmax warp leaves here)
-            if (ptx::named_barrier_or(2, soft_threads, dead)) goto softmax_done;
+            ptx::named_barrier(2, soft_threads);
             tc::fence_after_sync();
             {
                 float M = mref, L = l, w0 = 1.f, w1 = 0.f;
@@ -999,7 +997,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
             }
             tc::fence_before_sync();
         }
-    softmax_done:;
     }
     tc::fence_before_sync();
     __syncthreads();
