@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <limits>
 
 #include "device_common.cuh"
 #include "encode.cuh"
@@ -444,9 +445,15 @@ tq_status tq_rope_init(int32_t rotary_dims, int32_t layout, double base, int32_t
     if (banded && !(std::isfinite(low) && std::isfinite(high) && low > 0.0 && high > low &&
                     std::isfinite(trained_len) && trained_len > 0.0))
         return TQ_ERR_INVALID_ARG;
+    // The frequencies in 64-bit significands: a table entry is right to about
+    // its last bit, 2^-64 of a turn, and its product with any int32 position to
+    // 2^-32 (a double's would be off by 2^-25 there).
+    using wide = long double;
+    static_assert(std::numeric_limits<wide>::digits >= 64, "a table entry needs 64 bits");
     const double r = rotary_dims, two_pi = 2.0 * M_PI;
-    double b = base;
-    if (scaling == TQ_ROPE_SCALE_BASE && rotary_dims > 2) b *= std::pow(factor, r / (r - 2.0));
+    const wide turn = 6.28318530717958647692528676655900577L;
+    wide b = base;
+    if (scaling == TQ_ROPE_SCALE_BASE && rotary_dims > 2) b *= std::pow(wide(factor), wide(r) / (r - 2.0));
     double lo = 0.0, hi = 0.0;
     if (scaling == TQ_ROPE_SCALE_RAMP) {
         // the pairs that turn `high` and `low` times within the trained length
@@ -459,22 +466,22 @@ tq_status tq_rope_init(int32_t rotary_dims, int32_t layout, double base, int32_t
     t.magnitude = magnitude > 0.0 ? magnitude
                   : scaling == TQ_ROPE_SCALE_RAMP ? std::fmax(1.0, 0.1 * std::log(factor) + 1.0) : 1.0;
     for (int i = 0; i < rotary_dims / 2; ++i) {
-        double f = std::pow(b, -2.0 * i / r);
+        wide f = std::pow(b, wide(-2.0) * i / r);
         if (scaling == TQ_ROPE_SCALE_LINEAR) {
             f /= factor;
         } else if (scaling == TQ_ROPE_SCALE_WAVELENGTH) {
-            const double s = std::fmin(1.0, std::fmax(0.0, (trained_len * f / two_pi - low) / (high - low)));
-            f = (1.0 - s) * f / factor + s * f;
+            const wide s = std::fmin(wide(1), std::fmax(wide(0), (trained_len * f / turn - low) / (wide(high) - low)));
+            f = (1.0L - s) * f / factor + s * f;
         } else if (scaling == TQ_ROPE_SCALE_RAMP) {
-            const double s = std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 0.001)));
-            f = s * f / factor + (1.0 - s) * f;
+            const wide s = std::fmin(wide(1), std::fmax(wide(0), wide(i - lo) / std::fmax(hi - lo, 0.001)));
+            f = s * f / factor + (1.0L - s) * f;
         }
-        if (!std::isfinite(f)) return TQ_ERR_INVALID_ARG;
-        // turns per position, modulo one, in 2^-64ths (below 2^53 whole turns: f / 2 pi is exact to its last bit)
-        double turns = f / two_pi;
+        if (!std::isfinite(static_cast<double>(f))) return TQ_ERR_INVALID_ARG;
+        // turns per position, modulo one, in 2^-64ths
+        wide turns = f / turn;
         turns -= std::floor(turns);
-        const double hi32 = std::floor(std::ldexp(turns, 32));
-        const double rest = std::nearbyint(std::ldexp(std::ldexp(turns, 32) - hi32, 32));
+        const wide hi32 = std::floor(std::ldexp(turns, 32));
+        const wide rest = std::nearbyint(std::ldexp(std::ldexp(turns, 32) - hi32, 32));
         t.turns[i] = (static_cast<uint64_t>(hi32) << 32) + static_cast<uint64_t>(rest);
     }
     *out = t;
