@@ -257,6 +257,12 @@ class CacheTensors:
     v_norms: torch.Tensor
     qjl_matrix: torch.Tensor
 
+    def __post_init__(self):
+        # (checked here once: the calls look at k_codes alone)
+        if len({t.device for t in (self.k_codes, self.k_norms, self.k_qjl, self.k_gamma, self.v_codes, self.v_norms,
+                                   self.qjl_matrix) if t is not None}) > 1:
+            raise ValueError("a cache's arrays are on more than one device")
+
     def struct(self):
         return tq_cache(self.batch, self.capacity, _ptr(self.k_codes), _ptr(self.k_norms), _ptr(self.k_qjl),
                         _ptr(self.k_gamma), _ptr(self.v_codes), _ptr(self.v_norms), _ptr(self.qjl_matrix))
@@ -588,6 +594,8 @@ class draft_layers:
         self.layers = list(layers)
         if not self.layers:
             raise ValueError("at least one layer is wanted")
+        if len({c.k_codes.device for _, c in self.layers}) > 1:
+            raise ValueError("the layers' caches are on more than one device")
         self.tensors = [list(vars(c).values()) for _, c in self.layers]  # (whose addresses the structs hold)
         n = len(self.layers)
         self.params = (tq_params * n)(*[p for p, _ in self.layers])
