@@ -447,7 +447,11 @@ def _code(t):
 
 
 def _stream_for(stream, *tensors):
-    """The handle of the stream (None: torch's current one); the call's tensors lie on the current device, as does it."""
+    """The handle of the stream (None: torch's current one); the call's tensors, the error word last, lie on the current
+    device, as does it."""
+    error = tensors[-1]
+    if error is not None and (error.element_size() != 4 or error.numel() < 1):
+        raise ValueError("error: a tensor of a 32-bit type is wanted")
     device = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != device:
