@@ -586,11 +586,12 @@ tq_status tq_rope_append_paged(const tq_params* params, const tq_codebook* kcb, 
  * entry outside the pool sets TQ_DEVERR_PAGE; that sequence's output is not
  * valid.  sparse_v_threshold is not applied.  Every configuration of
  * tq_params is taken; outputs are within 2e-3 (relative L2 per row) of exact
- * attention over the stored codes, plus the rounding to out_dtype.  (bf16
- * outputs take their queries in 11 bits of each entry, the others in about 22
- * of the row's largest entry, whatever its size.  Turbo values
- * of d = 128 layers without a sketch are rounded at one scale for all norms,
- * which adds up to 2^-22 (L2) to a row, whatever its size.)
+ * attention over the stored codes, plus the rounding to out_dtype, where scores
+ * are of ordinary size: the fp16 operands (the key table, and queries of 11 bits
+ * for bf16 outputs; the others take about 22) move a score by about 6e-5 (2e-4
+ * for bf16 outputs) of sm_scale |q| |k| / sqrt(d), so beyond 8 (2.5) of that the
+ * error grows with it.  Turbo values of d = 128 layers without a sketch are
+ * rounded at one scale for all norms, which adds up to 2^-22 (L2) to a row.
  * TQ_ERR_UNSUPPORTED also where the device reserves another amount of shared
  * memory per block than 1 KB (d = 128 without a sketch).
  */

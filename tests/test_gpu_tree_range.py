@@ -1,16 +1,17 @@
 """Tree attention over the whole range of what a cache and its queries may
 hold, against the plain fp64 reference of drafts_ref.py: value scales and
 norms from the smallest to the largest that fp16 stores, queries far from one,
-slots at the end of the int32 range.  Tolerances as in test_gpu_drafts.py: 2e-3 relative L2
-per row and the rounding of the output.
+softmax references that have to be raised again and again, long contexts,
+slots at the end of the int32 range.  Tolerances as in test_gpu_drafts.py:
+2e-3 relative L2 per row and the rounding of the output.
 
 The 2e-3 covers what the operands round.  A score is a sum of d products of
 about |q| |k| / d each, so an error e of each (independent) moves it by
 e |q| |k| sm / sqrt(d): here |q| |k| sm is at most 120 (keys of norm 30 with
 lognormal channels, times 4 where norms grow), so the key table's 6e-5 (rms
 of the 4-bit table in fp16) move a weight by 6.4e-4 of itself, and a query in
-11 bits (2^-12.8 rms, bf16 outputs only, whose tolerance has 2^-8 more) by
-1.5e-3; weights and values in fp16 add 2^-12.8 each."""
+11 bits (2^-12.3 rms, bf16 outputs only, whose tolerance has 2^-8 more) by
+5e-4, or 2.1e-3 where norms grow; weights and values in fp16 add 2^-12.8 each."""
 
 import numpy as np
 import pytest
@@ -18,7 +19,7 @@ import torch
 
 import drafts_ref as R
 from bit_kv_cache_tq_b200 import tq
-from test_gpu_drafts import BF16, FP32, _check_rows, _layer, _tree_call
+from test_gpu_drafts import BF16, FP16, FP32, _check_rows, _layer, _tree_call
 
 pytestmark = pytest.mark.gpu
 
@@ -114,6 +115,69 @@ def test_queries_at_the_ends_of_fp32(d, kb, power):
     q = torch.randn(1, 9, 4, d, generator=torch.Generator().manual_seed(3)) * 2.0 ** power
     for dtype in (FP32, BF16):
         _check_rows(*_run(layer, cache, q.to(dtype), mask, [0], 9, dtype), dtype)
+
+
+# --------------------------------------------------------------- references
+RAISE = [  # d, hq, hkv, kb, vb, qjl, base, drafts, dtype: one and two terms, paired and not, whole units and pieces
+    (128, 8, 1, 4, 2, 0, 3000, 30, BF16),
+    (128, 8, 2, 4, 2, 0, 3000, 30, BF16),
+    (128, 8, 2, 4, 4, 0, 3000, 30, FP16),
+    (128, 4, 1, 3, 3, 0, 3000, 30, FP32),
+    (128, 8, 1, 8, 8, 0, 3000, 30, BF16),
+    (64, 8, 2, 4, 2, 0, 1500, 30, BF16),
+    (128, 8, 2, 3, 2, 32, 1500, 30, FP32),
+    (256, 8, 2, 4, 2, 0, 1500, 30, FP16),
+]
+
+
+@pytest.mark.parametrize("few_blocks", [False, True])
+@pytest.mark.parametrize("d,hq,hkv,kb,vb,qjl,base,drafts,dtype", RAISE)
+def test_references_raised_tile_after_tile(d, hq, hkv, kb, vb, qjl, base, drafts, dtype, few_blocks):
+    """Keys whose norms grow along the context, so that every row's largest score rises over its tiles; many sequences
+    (few_blocks) leave each block whole units, so that one stream sees the whole rise."""
+    layer = _layer(d, hq, hkv, kb, vb, qjl, seed=6)
+    batch = 160 if few_blocks else 1
+    if few_blocks:
+        base = 500
+    total = base + drafts
+    cache, _ = R.make_cache(layer, batch, total + 2)
+    one, _ = R.make_cache(layer, 1, total + 2)
+    R.fill(layer, one, None, 1, total, seed=2)
+    grow = torch.linspace(0.1, 4.0, total + 2, device="cuda")
+    _half(one.k_norms).mul_(grow.half())
+    for name in ("k_codes", "k_norms", "k_qjl", "k_gamma", "v_codes", "v_norms"):
+        if getattr(one, name) is not None:
+            getattr(cache, name).copy_(getattr(one, name).expand_as(getattr(cache, name)))
+    mask = R.random_tree(1, drafts, seed=5)
+    q = torch.randn(1, drafts, hq, d, generator=torch.Generator().manual_seed(3)).to(dtype)
+    qs, masks = q.expand(batch, -1, -1, -1).contiguous(), np.repeat(mask, batch, 0)
+    out = torch.full(qs.shape, 7.0, dtype=dtype, device="cuda")
+    err = _tree_call(layer, qs.cuda(), torch.from_numpy(masks).cuda(), [base] * batch, cache, None, out)
+    assert tq.tq_read_device_error(err) == (tq.TQ_OK, 0)
+    want = R.tree_attention(layer, one, q.double().numpy(), mask, [base], [drafts])
+    # bf16 outputs take their queries in 11 bits: an entry is off by 2^-12.3 of itself (rms: uniform within half a step,
+    # the mantissa spread evenly), a score by 2^-12.3 sm |q| |k| / sqrt(d), independent from key to key; of the scores
+    # of a row that share its weight, none is off by more than 4.5 such (15 million draws), so no weight by more than
+    # twice that against its row's others
+    tol = R.H.ATTN_TOL + R.EPS[dtype]
+    if dtype == BF16:
+        k = max(np.linalg.norm(R.H.stored_hat(layer, one, 0, h, total, 0), axis=-1).max() for h in range(hkv))
+        tol += 9 * 2.0 ** -12.3 * q.double().norm(dim=-1).max().item() * k / d
+    for b in {0, batch // 2, batch - 1}:
+        assert R.H.rel_l2_per_vector(out[b:b + 1].cpu().double().numpy(), want).max() <= tol
+
+
+@pytest.mark.parametrize("d,hq,kb,vb,qjl,dtype", [(128, 16, 4, 2, 0, BF16), (128, 4, 3, 4, 0, FP32),
+                                                  (128, 4, 3, 2, 64, BF16), (64, 4, 4, 8, 0, BF16)])
+def test_a_long_context(d, hq, kb, vb, qjl, dtype):
+    """40000 slots of one kv head."""
+    layer = _layer(d, hq, 1, kb, vb, qjl, seed=6)
+    base, n = 40000, 20
+    cache, _ = R.make_cache(layer, 1, base + n)
+    R.fill(layer, cache, None, 1, base + n, seed=2)
+    mask = R.random_tree(1, n, seed=5)
+    q = torch.randn(1, n, hq, d, generator=torch.Generator().manual_seed(3)).to(dtype)
+    _check_rows(*_run(layer, cache, q, mask, [base], n, dtype), dtype)
 
 
 # ---------------------------------------------------------------- positions
