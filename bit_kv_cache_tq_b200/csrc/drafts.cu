@@ -103,12 +103,17 @@ __device__ __forceinline__ void move_codes(const Layer& y, const long long* from
 // Block (sequence and two heads, layer).  It is latency: a chain of length,
 // path, row and write; two heads a block share the chain's start, and six
 // blocks an SM cover one another's.  (48 sequences x 32 layers x 8 heads, up to
-// 64 rows of 116 bytes each: 27 us, 3.3 TB/s, a norm's 2 bytes costing a sector
-// of 32 each way; 27.5 us with four heads a block and four blocks an SM, 42 with
-// one head, 67 with one head and divisions in the row index.)
+// 64 rows of 116 bytes each: 27 us, 3.3 TB/s.  Its 6144 blocks each walk the
+// chain anew, barriers being the first stall; of the 64 MB it reads, 44 are the
+// rows, the rest mostly the second halves of 48-byte rows' sectors and sectors
+// written in part; norms, next to each other, are 5%.  27.5 us with four heads a
+// block and four blocks an SM, 42 with one head, 67 with one head and divisions
+// in the row index.)
 // SMALL: every layer's rows are of at most 64 bytes, in 16-byte units; SKETCH:
 // some layer has one (the larger rows' and the sketches' registers would cost
-// the others their blocks per SM).
+// the others their blocks per SM).  One layer with wider rows sends a launch's
+// layers all to the wide instance: the same call with four int8 layers takes 83
+// us in place of 30 (caches flushed).
 template <bool SMALL, bool SKETCH>
 __global__ void __launch_bounds__(THREADS, SMALL ? (SKETCH ? 3 : 6) : 1) commit_kernel(const __grid_constant__ Args a) {
     __shared__ long long from[MAX_PATH], to[MAX_PATH];  // cache rows of head 0 (from: -1, a row that stays)

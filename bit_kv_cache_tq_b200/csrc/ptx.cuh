@@ -211,8 +211,6 @@ __device__ __forceinline__ uint2 lds64_imm(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ float lds_f32(uint32_t addr) { return __uint_as_float(lds32(addr)); }
-
 __device__ __forceinline__ uint16_t lds16(uint32_t addr) {
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));

@@ -17,7 +17,11 @@
 // It is bound by instructions where it quantises and by memory where it turns
 // queries, so blocks of the three kinds of work alternate.  8192 tokens of
 // 32 + 8 + 8 heads, K4/V3, bf16: 54 us (176 MB, 3.3 TB/s), quantising alone
-// 24.
+// 24.  (The kinds share one register limit, 80 for three blocks an SM, at which
+// the encoders spill 284 bytes.  With cold caches: 62 us, int8 sides 50, keys with
+// 64 sketch rows 193, whose search and sketch are scalar; rotary_dims other than d
+// and d/2 in the half layout cost 45 us more, the partners being read again one by
+// one.)
 
 #include <cuda_runtime.h>
 

@@ -19,10 +19,11 @@
 // worked on.  Queries enter as fp16 terms: two, so that a score keeps
 // about 22 bits of its query, or one for bf16 outputs (see the other kernel).  The key axis is split between blocks and the
 // merge kernel joins the pieces.  It is bound by the latency of that chain with
-// three blocks an SM (two at d = 256), about 3000 instructions a warp and tile:
-// 16 drafts of 32 heads over 6000 tokens take 63 us at d = 256 and 51 at d = 128
-// with a sketch; 4 sequences of 777 to 4001 tokens, 17 drafts of 16 heads, int8,
-// d = 64: 33 us.
+// three blocks an SM (two at d = 256): 2800 instructions a warp and tile of 32
+// keys at d = 256, in 27% of the issue slots, 1500 a tile of 64 in 35% at d = 64;
+// the first stalls are fixed latencies and instruction fetch.  16 drafts of 32
+// heads over 6000 tokens take 68 us at d = 256 and 55 at d = 128 with a sketch; 4
+// sequences of 777 to 4001 tokens, 17 drafts of 16 heads, int8, d = 64: 34 us.
 
 #include "tree_common.cuh"
 #include "tree_mma_impl.cuh"

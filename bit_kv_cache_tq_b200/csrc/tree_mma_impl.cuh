@@ -54,9 +54,20 @@
 // of ten.)  A pair of row blocks takes about 3400 cycles a tile, of which the
 // tensor cores work 1020: the chain scores, softmax, weights, P V of a stream
 // is longer than the other stream can cover.  64 drafts of 32 heads over 32768
-// tokens (K4/V2, 8 kv heads, bf16): 90 us, 382 TFLOP/s; 16 sequences of 2048 to
-// 8192 tokens in pages, 13 drafts each (K3/V2): 114 us; 2 x 131072 tokens, 25
-// drafts of 64 heads (K4/V4, fp16, two terms): 470 to 520 us.
+// tokens (K4/V2, 8 kv heads, bf16): 89 us, 385 TFLOP/s; 16 sequences of 2048 to
+// 8192 tokens in pages, 13 drafts each (K3/V2): 113 us; 2 x 131072 tokens, 25
+// drafts of 64 heads (K4/V4, fp16, two terms): 507 to 516 us.
+// Units of few rows are bound elsewhere: with 52 rows a stream's softmax is two
+// warps, and both streams' are on the same two of the SM's four sub-partitions
+// (the busiest one issues 2.5 times the instructions of the idlest, 39% of the
+// slots on average), at 2700 cycles a tile of which the MMAs, half of their rows
+// empty, take 600.
+//
+// What is rounded to fp16, and why that is enough: the key table (at the scale
+// that rounds it best, 6e-5 of an entry), a value row (table times norm, 2^-12.3
+// rms), a weight (the same), the queries in one or two terms.  Products and sums
+// are fp32.  Together 4.5e-4 of a row over 131072 tokens, fp16 outputs' own
+// rounding of 2.1e-4 included.
 //
 // Every mbarrier wait is bounded (about a second, then TQ_DEVERR_TIMEOUT; the
 // block stops issuing copies and MMAs, waits for those under way, and its other
@@ -143,6 +154,7 @@ __host__ __device__ constexpr uint32_t sm_alloc(int kb, int vb) {
 static_assert(sm_alloc(4, 4) <= 227u * 1024u && sm_alloc(4, 8) <= 227u * 1024u && sm_alloc(8, 8) <= 227u * 1024u,
               "the largest layouts fit a block's shared memory");
 
+__device__ __forceinline__ float lds_f32(uint32_t addr) { return __uint_as_float(ptx::lds32(addr)); }
 __device__ __forceinline__ uint32_t pack2(uint16_t lo, uint16_t hi) { return lo | (static_cast<uint32_t>(hi) << 16); }
 
 // ------------------------------------------------------------ the schedule
@@ -784,10 +796,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                 // sum (one straight run of code without the mask's test and the
                 // rows' factors)
                 auto weigh = [&](auto with_mask) {
-                    const float f = decltype(with_mask)::value ? ptx::lds_f32(sbase + SM_FACTOR + 4 * tid) : 1.f;
+                    const float f = decltype(with_mask)::value ? lds_f32(sbase + SM_FACTOR + 4 * tid) : 1.f;
                     const uint64_t seen = decltype(with_mask)::value ? visible(mask, key0, x.base) : 0ull;
                     const uint32_t vis[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
-                    const float shift = (VB == 8 ? WSHIFT + ptx::lds_f32(ve) : WSHIFT) - mref;
+                    const float shift = (VB == 8 ? WSHIFT + lds_f32(ve) : WSHIFT) - mref;
                     const float2 nm2 = make_float2(shift, shift);
                     float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
                     float sc[32];
@@ -841,7 +853,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     // a weight may leave the fp16 range (or is NaN): raise the
                     // reference to the row's largest score, rescale, again
                     float m = -INFINITY;
-                    const float f = ptx::lds_f32(sbase + SM_FACTOR + 4 * tid);
+                    const float f = lds_f32(sbase + SM_FACTOR + 4 * tid);
                     const uint64_t seen = careful ? visible(mask, key0, x.base) : ~0ull;
 #pragma unroll 1
                     for (int h = 0; h < 4; ++h) {
@@ -855,7 +867,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                             if ((v >> i) & 1u) m = fmaxf(m, __fmul_rn(__fmul_rn(sc[i], f), n));
                         }
                     }
-                    const float mnew = fmaxf(VB == 8 ? m + ptx::lds_f32(ve) : m, mref), c = ptx::ex2(mref - mnew);
+                    const float mnew = fmaxf(VB == 8 ? m + lds_f32(ve) : m, mref), c = ptx::ex2(mref - mnew);
                     // (past 2^22 a fused product would differ from the reference by more than a bit)
                     if (__any_sync(kFullMask, fabsf(mnew) > 0x1p22f && mnew > NOTHING)) careful_from = -1;
                     if (!first) {
@@ -877,7 +889,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tree_mma_kernel(const __grid_cons
                     l *= c;
                     mref = mnew;
                 }
-                l += VB == 8 ? sum * ptx::lds_f32(ve + 4) : sum;
+                l += VB == 8 ? sum * lds_f32(ve + 4) : sum;
                 uint32_t pd = tmem + lanes + TM_S + BK * g;
                 if (!overlay) {
                     tc::fence_before_sync();
