@@ -858,8 +858,12 @@ static tq_status attend(const tq_params* params, const tq_codebook* kcb, const t
     // key centroids enter at the codebook's fp16 scale, which rounds the table
     // best; the values' as sqrt(d)/4 c or q / 128, below one (times a norm they stay
     // below the fp16 range)
-    const double ak = a.k_bits == 8 ? 1.0 / 128.0
-                                    : (kcb->fp16_scale > 0.0 ? kcb->fp16_scale : rd) * (mm ? mma::KEY_SHIFT : 1.0);
+    double ak = 1.0 / 128.0;
+    if (a.k_bits < 8) {
+        ak = kcb->fp16_scale > 0.0 ? kcb->fp16_scale : rd;
+        int e;
+        if (mm) ak = std::frexp(ak, &e) * 16.0 * mma::KEY_SHIFT;  // (a caller's scale brought to [8, 16) too)
+    }
     a.key_scale = static_cast<float>(ak);
     a.score_scale = static_cast<float>(sm * 1.4426950408889634 / ak);
     // (the tensor-memory kernel rounds the value table itself to fp16: at its codebook's scale too)

@@ -212,3 +212,18 @@ def test_drafts_in_the_last_tile_of_the_int32_range():
         err = _tree_call(layer, q.to(dtype).cuda(), mask.cuda(), [base], pool, table, out)
         assert tq.tq_read_device_error(err) == (tq.TQ_OK, 0)
         _check_rows(out, want, dtype)
+
+
+@pytest.mark.parametrize("power", [-6, 5])
+def test_a_codebook_scale_of_the_callers(power):
+    """The scale of the fp16 tables is the caller's to choose; a power of two of the usual one rounds the keys the same."""
+    layer = _layer(128, 8, 2, 4, 8, seed=6)
+    cache, _ = R.make_cache(layer, 1, 230)
+    R.fill(layer, cache, None, 1, 230, seed=2)
+    mask = R.random_tree(1, 20, seed=5)
+    q = torch.randn(1, 20, 8, 128, generator=torch.Generator().manual_seed(3))
+    out, _ = _run(layer, cache, q, mask, [200], 20, FP32)
+    layer.kcb.fp16_scale *= 2.0 ** power
+    again, want = _run(layer, cache, q, mask, [200], 20, FP32)
+    _check_rows(again, want, FP32)
+    assert torch.equal(out, again)
